@@ -23,17 +23,21 @@ for its size (``kda_chunk_fwd_workspace_size`` / ``kda_varlen_fwd_workspace_size
 and allocate it with PyTorch's caching allocator, or take a caller's uint8
 ``workspace`` tensor.  ``cuda_cores=True`` runs the fp32 CUDA-core kernel and
 ``blocks=n`` the two-stream blocked schedule (cross-checks; same results).
+
+The short causal convolution (``kda_conv_*``) and the selective state space scan
+(``kda_ssm_*``) for prompts, single tokens and training are in ``mixer``.
 """
 from __future__ import annotations
 
 import torch
 
-from . import _lib
+from . import _lib, mixer
 from ._lib import KdaError
+from .mixer import *  # noqa: F401,F403
 
 __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_varlen_fwd", "kda_recurrent_step", "kda_check",
            "kda_chunk_bwd", "kda_varlen_bwd", "kda_dplr_fwd", "kda_dplr_varlen_fwd", "chunk_fwd_workspace_size",
-           "varlen_fwd_workspace_size", "dplr_fwd_workspace_size", "KdaError"]
+           "varlen_fwd_workspace_size", "dplr_fwd_workspace_size", "KdaError", *mixer.__all__]
 
 _DTYPES = {torch.float32: _lib.KDA_F32, torch.bfloat16: _lib.KDA_BF16}
 

@@ -16,6 +16,8 @@ KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_TIMEOUT,
 KDA_F32, KDA_BF16 = 0, 1
 KDA_MODE_HEAD_GATE, KDA_MODE_NO_ERASE, KDA_MODE_NORM_QK, KDA_MODE_GATE_LOGITS = 1, 2, 4, 8
 KDA_MODE_CUDA_CORES = 16
+KDA_CONV_SILU = 1
+KDA_SSM_SOFTPLUS = 1
 
 
 def KDA_MODE_BLOCKS(n: int) -> int:
@@ -27,6 +29,8 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
 _ZP = ctypes.POINTER(ctypes.c_size_t)
+_L = ctypes.c_longlong
+_SSM_IN = [_P, _L, _P, _L, _P, _P, _L, _P, _L, _P, _P, _L, _P]   # x dt A B C skip z dt_bias, with row strides
 SIGNATURES = {
     "kda_chunk_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _Z, _P]),
     "kda_chunk_fwd_workspace_size": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, _ZP]),
@@ -46,6 +50,21 @@ SIGNATURES = {
     "kda_dplr_fwd_workspace_size": (_I, [_I] * 7 + [_ZP]),
     "kda_dplr_varlen_fwd": (_I, [_P] * 7 + [_I] + [_P] * 3 + [_I] * 7 + [_P, _Z, _P]),
     "kda_dplr_varlen_fwd_workspace_size": (_I, [_I] * 7 + [_ZP]),
+    "kda_conv_fwd": (_I, [_P, _L] + [_P] * 5 + [_I] * 7 + [_P]),
+    "kda_conv_varlen_fwd": (_I, [_P, _L] + [_P] * 3 + [_I] + [_P] * 3 + [_I] * 6 + [_P]),
+    "kda_conv_step": (_I, [_P, _L] + [_P] * 4 + [_I] * 6 + [_P]),
+    "kda_conv_bwd": (_I, [_P, _L] + [_P] * 9 + [_I] * 6 + [_P, _Z, _P]),
+    "kda_conv_varlen_bwd": (_I, [_P, _L] + [_P] * 3 + [_I] + [_P] * 7 + [_I] * 5 + [_P, _Z, _P]),
+    "kda_conv_bwd_workspace_size": (_I, [_L, _I, _I, _ZP]),
+    "kda_ssm_fwd": (_I, _SSM_IN + [_P] * 3 + [_I] * 8 + [_P, _Z, _P]),
+    "kda_ssm_fwd_workspace_size": (_I, [_I] * 6 + [_ZP]),
+    "kda_ssm_varlen_fwd": (_I, _SSM_IN + [_P, _I] + [_P] * 3 + [_I] * 7 + [_P, _Z, _P]),
+    "kda_ssm_varlen_fwd_workspace_size": (_I, [_I] * 6 + [_ZP]),
+    "kda_ssm_step": (_I, _SSM_IN + [_P] * 2 + [_I] * 7 + [_P]),
+    "kda_ssm_bwd": (_I, _SSM_IN + [_P] * 12 + [_I] * 7 + [_P, _Z, _P]),
+    "kda_ssm_bwd_workspace_size": (_I, [_I] * 6 + [_ZP]),
+    "kda_ssm_varlen_bwd": (_I, _SSM_IN + [_P, _I] + [_P] * 12 + [_I] * 6 + [_P, _Z, _P]),
+    "kda_ssm_varlen_bwd_workspace_size": (_I, [_I] * 6 + [_ZP]),
     "kda_check": (_I, [_P]),
     "kda_selftest_timeout": (_I, [ctypes.c_longlong, _P]),
     "kda_status_string": (ctypes.c_char_p, [_I]),

@@ -7,3 +7,7 @@
 #include "kda_chunk_split.cu"
 #include "kda_chunk_bwd.cu"
 #include "kda_dplr.cu"
+#include "kda_mixer_api.cu"
+#include "kda_conv.cu"
+#include "kda_ssm.cu"
+#include "kda_ssm_bwd.cu"

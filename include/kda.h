@@ -359,6 +359,161 @@ kda_status kda_dplr_varlen_fwd_workspace_size(int N, int T, int H, int dk, int d
                                               size_t* bytes);
 
 /*
+ * Short causal depthwise convolution, the token mixer in front of the layer's
+ * q, k, v projections and of the selective scan below.  Per channel d:
+ *
+ *     pre[t, d] = bias[d] + sum_{j < W} weight[d, j] * x[t - W + 1 + j, d]
+ *     y[t, d]   = pre, or silu(pre) = pre * sigmoid(pre) with KDA_CONV_SILU
+ *
+ * (tap W - 1 is the current token).  Inputs before a sequence's first token
+ * come from its state, the last W - 1 inputs, oldest first; a missing initial
+ * state is zero.  fp32 arithmetic; y is rounded once, to o_dtype.
+ *
+ *   x        rows of D elements of type `dtype`, row (b, t) at x + (b T + t) ldx:
+ *            ldx >= D elements, a multiple of 16 bytes (D for a dense tensor),
+ *            so x may be a column slice of a wider projection
+ *   weight   [D, W] fp32; bias [D] fp32 or NULL; 16-byte aligned
+ *   initial_state / final_state [N, W - 1, D] of type `dtype` or NULL (final may
+ *            be the same memory as initial); copies of inputs, never rounded
+ *   y        [B, T, D] (dense) or [T, D] (packed), o_dtype, written
+ *   mode     0 or KDA_CONV_SILU
+ * D a multiple of 8, at most 2^20, W in {2, 3, 4}: others return
+ * KDA_ERR_UNSUPPORTED.  Packed batches follow kda_varlen_fwd's rules: a sequence
+ * outside [0, T) is skipped and reported by kda_check(), y rows of no sequence
+ * are not written.  Needs no workspace.
+ */
+#define KDA_CONV_SILU 1
+
+kda_status kda_conv_fwd(const void* x, long long ldx, const float* weight, const float* bias,
+                        const void* initial_state, void* y, void* final_state,
+                        int B, int T, int D, int W, kda_dtype dtype, kda_dtype o_dtype, int mode, void* stream);
+
+kda_status kda_conv_varlen_fwd(const void* x, long long ldx, const float* weight, const float* bias,
+                               const int32_t* cu_seqlens, int N, const void* initial_state, void* y,
+                               void* final_state, int T, int D, int W, kda_dtype dtype, kda_dtype o_dtype, int mode,
+                               void* stream);
+
+/* One token for each of N sequences: x rows n at x + n ldx, y [N, D],
+ * state [N, W - 1, D] read and moved on by one token in place. */
+kda_status kda_conv_step(const void* x, long long ldx, const float* weight, const float* bias, void* state, void* y,
+                         int N, int D, int W, kda_dtype dtype, kda_dtype o_dtype, int mode, void* stream);
+
+/*
+ * Gradients of L = sum(y * grad_y) + sum(final_state * grad_final_state):
+ *   grad_y [B, T, D] fp32; grad_final_state [B, W - 1, D] fp32 or NULL (zero)
+ *   grad_x [B, T, D] fp32, grad_weight [D, W] fp32, written
+ *   grad_bias [D] fp32, grad_initial_state [B, W - 1, D] fp32, or NULL if not wanted
+ *   workspace  at least kda_conv_bwd_workspace_size() bytes, 256-byte aligned
+ *              (partial sums of the weight's gradient, added in a fixed order)
+ * Packed batches: rows of no sequence and of skipped ones get a zero grad_x, a
+ * skipped sequence's grad_initial_state is grad_final_state.  The gradient
+ * buffers must not alias the inputs.
+ */
+kda_status kda_conv_bwd(const void* x, long long ldx, const float* weight, const float* bias,
+                        const void* initial_state, const float* grad_y, const float* grad_final_state,
+                        float* grad_x, float* grad_weight, float* grad_bias, float* grad_initial_state,
+                        int B, int T, int D, int W, kda_dtype dtype, int mode, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+kda_status kda_conv_varlen_bwd(const void* x, long long ldx, const float* weight, const float* bias,
+                               const int32_t* cu_seqlens, int N, const void* initial_state, const float* grad_y,
+                               const float* grad_final_state, float* grad_x, float* grad_weight, float* grad_bias,
+                               float* grad_initial_state, int T, int D, int W, kda_dtype dtype, int mode,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of both backward calls for `tokens` tokens in all (B * T). */
+kda_status kda_conv_bwd_workspace_size(long long tokens, int D, int W, size_t* bytes);
+
+/*
+ * Selective state space scan: the recurrence with one decay per (channel, state
+ * index).  Per channel d of group g (D / G channels each), with S states:
+ *
+ *     Delta_t  = softplus(dt[t, d] + dt_bias[d])       (KDA_SSM_SOFTPLUS; else the sum itself)
+ *     h_t[s]   = exp(Delta_t A[d, s]) h_{t-1}[s] + Delta_t x[t, d] B[t, g, s]
+ *     y[t, d]  = (sum_s C[t, g, s] h_t[s] + skip[d] x[t, d]) * silu(z[t, d])
+ *
+ * without the skip term, the gate or the bias where skip, z or dt_bias is NULL.
+ * (With one decay per head instead, the recurrence is this library's layer with
+ * KDA_MODE_HEAD_GATE | KDA_MODE_NO_ERASE.)  fp32 arithmetic and state.
+ *
+ *   x, dt, z   rows of D elements, B, C rows of G * S elements, all of type
+ *              `dtype`; row (b, t) at pointer + (b T + t) * its ld, ld in elements,
+ *              a multiple of 16 bytes, at least the row's length
+ *   A          [D, S] fp32, <= 0 (not checked); skip, dt_bias [D] fp32 or NULL
+ *   initial_state / final_state [N, D, S] fp32 or NULL (final may be the same
+ *              memory as initial)
+ *   y          [B, T, D] (dense) or [T, D] (packed), o_dtype, written
+ *   mode       0 or KDA_SSM_SOFTPLUS
+ *   workspace  at least the *_workspace_size() bytes, 256-byte aligned, contents
+ *              need no initialisation; NULL when that size is 0
+ * D a multiple of 8 * G, at most 2^20, S in {16, 32, 64}: others return
+ * KDA_ERR_UNSUPPORTED.  Pointers 16-byte aligned.  Packed batches follow
+ * kda_varlen_fwd's rules (skipped sequences: y rows not written, final state =
+ * initial state; rows of no sequence not written).
+ */
+#define KDA_SSM_SOFTPLUS 1
+
+kda_status kda_ssm_fwd(const void* x, long long ldx, const void* dt, long long lddt, const float* A,
+                       const void* B_, long long ldb, const void* C_, long long ldc, const float* skip,
+                       const void* z, long long ldz, const float* dt_bias, const float* initial_state,
+                       void* y, float* final_state, int B, int T, int D, int S, int G,
+                       kda_dtype dtype, kda_dtype o_dtype, int mode, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+kda_status kda_ssm_fwd_workspace_size(int B, int T, int D, int S, int G, kda_dtype dtype, size_t* bytes);
+
+kda_status kda_ssm_varlen_fwd(const void* x, long long ldx, const void* dt, long long lddt, const float* A,
+                              const void* B_, long long ldb, const void* C_, long long ldc, const float* skip,
+                              const void* z, long long ldz, const float* dt_bias, const int32_t* cu_seqlens, int N,
+                              const float* initial_state, void* y, float* final_state, int T, int D, int S, int G,
+                              kda_dtype dtype, kda_dtype o_dtype, int mode, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+kda_status kda_ssm_varlen_fwd_workspace_size(int N, int T, int D, int S, int G, kda_dtype dtype, size_t* bytes);
+
+/* One token for each of N sequences (rows n of x, dt, B, C, z; y [N, D]);
+ * state [N, D, S] fp32 updated in place.  Memory bound: the state is read once
+ * and written once.  Needs no workspace. */
+kda_status kda_ssm_step(const void* x, long long ldx, const void* dt, long long lddt, const float* A,
+                        const void* B_, long long ldb, const void* C_, long long ldc, const float* skip,
+                        const void* z, long long ldz, const float* dt_bias, float* state, void* y,
+                        int N, int D, int S, int G, kda_dtype dtype, kda_dtype o_dtype, int mode, void* stream);
+
+/*
+ * Gradients of L = sum(y * grad_y) + sum(final_state * grad_final_state) through
+ * kda_ssm_fwd, recomputed from its inputs:
+ *   grad_y [B, T, D] fp32, grad_final_state [B, D, S] fp32 or NULL (zero)
+ *   grad_x, grad_dt [B, T, D], grad_A [D, S], grad_B, grad_C [B, T, G, S] fp32, written
+ *   grad_skip [D], grad_z [B, T, D], grad_dt_bias [D] fp32: written, and required,
+ *              where skip, z, dt_bias are given; NULL where they are not
+ *   grad_initial_state [B, D, S] fp32, or NULL if not wanted
+ * Sums over tokens, channels and sequences are added in a fixed order.  Packed
+ * batches: gradient rows of no sequence and of skipped ones are zero, a skipped
+ * sequence's grad_initial_state is grad_final_state.  The gradient buffers must
+ * not alias the inputs.
+ */
+kda_status kda_ssm_bwd(const void* x, long long ldx, const void* dt, long long lddt, const float* A,
+                       const void* B_, long long ldb, const void* C_, long long ldc, const float* skip,
+                       const void* z, long long ldz, const float* dt_bias, const float* initial_state,
+                       const float* grad_y, const float* grad_final_state, float* grad_x, float* grad_dt,
+                       float* grad_A, float* grad_B, float* grad_C, float* grad_skip, float* grad_z,
+                       float* grad_dt_bias, float* grad_initial_state, int B, int T, int D, int S, int G,
+                       kda_dtype dtype, int mode, void* workspace, size_t workspace_bytes, void* stream);
+
+kda_status kda_ssm_bwd_workspace_size(int B, int T, int D, int S, int G, kda_dtype dtype, size_t* bytes);
+
+kda_status kda_ssm_varlen_bwd(const void* x, long long ldx, const void* dt, long long lddt, const float* A,
+                              const void* B_, long long ldb, const void* C_, long long ldc, const float* skip,
+                              const void* z, long long ldz, const float* dt_bias, const int32_t* cu_seqlens, int N,
+                              const float* initial_state, const float* grad_y, const float* grad_final_state,
+                              float* grad_x, float* grad_dt, float* grad_A, float* grad_B, float* grad_C,
+                              float* grad_skip, float* grad_z, float* grad_dt_bias, float* grad_initial_state,
+                              int T, int D, int S, int G, kda_dtype dtype, int mode, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+kda_status kda_ssm_varlen_bwd_workspace_size(int N, int T, int D, int S, int G, kda_dtype dtype, size_t* bytes);
+
+/*
  * Synchronises `stream` and reports (then clears) the current device's
  * status word: KDA_ERR_TIMEOUT if a device-side bounded wait ran out since the
  * last check, KDA_ERR_INVALID_ARG if a kernel found device-resident sequence
