@@ -106,12 +106,19 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
+__device__ __forceinline__ float rcp_approx(float x)   // 1 ulp
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // sigmoid(x) from one exponential and one reciprocal; 0 and 1 at the ends.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + exp2_approx(-kLog2e * x)); }
+__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + exp2_approx(-kLog2e * x)); }
 
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + exp2_approx(-kLog2e * x)); }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
 // d silu(x) / dx = s + x s (1 - s), s = sigmoid(x)
 __device__ __forceinline__ float silu_grad(float x)

@@ -6,11 +6,12 @@ namespace {
 
 constexpr int kMaxChannels = 1 << 20;
 
-// Row stride of a token-major input: whole 16-byte vectors, rows that do not overlap.
+// Row stride of a token-major input: whole 16-byte vectors, rows that do not
+// overlap, below 4 GiB.
 bool valid_ld(long long ld, long long row, kda_dtype dtype)
 {
     const long long per16 = dtype == KDA_BF16 ? 8 : 4;
-    return ld >= row && ld % per16 == 0 && ld <= 0x7fffffffLL;
+    return ld >= row && ld % per16 == 0 && ld < 1LL << 30;
 }
 
 bool opt_aligned16(const void* p) { return !p || aligned16(p); }

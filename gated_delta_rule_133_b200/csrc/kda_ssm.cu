@@ -21,151 +21,251 @@ struct WalkBwd {
     float *gz, *ckpt;
 };
 
-template <typename T, int N, int L, int CK>
-__global__ void __launch_bounds__(128)
-ssm_walk_kernel(const SsmDev p, const WalkBwd w)
+// Shape of a walk.  A block owns DT = 8 channels of a sequence.  A warp holds all
+// states of the channels, a channel's N states on L = 4 lanes, NPT = N / 4 states
+// each, and takes TK tokens at a time; W such warps take turns.
+template <int N_>
+struct Walk {
+    static constexpr int N = N_, W = 4, L = 4, NPT = N / L, DT = 32 / L, THREADS = 32 * W;
+    static constexpr int TK = 32 / NPT;                      // 32 decays in registers
+    static constexpr int R = L < TK ? L : TK, VP = TK / R;   // lanes of a channel that finish tokens, tokens of each
+    static constexpr int DUROW = DT + 2, YROW = DT;          // (Delta, u) of a token: rows on other banks
+};
+
+__device__ __forceinline__ void bar_sync(int id, int threads)
 {
-    using K = Walk<T, N, L>;
-    constexpr int TT = K::TT, DT = K::DT, NPT = K::NPT, EP = K::EP;
-    extern __shared__ __align__(16) unsigned char smem[];
-    float* sDU = reinterpret_cast<float*>(smem + 2 * K::STAGE);
-    float* sB = sDU + TT * K::DUROW;
-    float* sC = sB + TT * N;
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Row t of an array with rows `bytes` apart: one wide multiply-add, and no pointer
+// is kept in registers.
+template <typename E>
+__device__ __forceinline__ const E* row(const void* base, unsigned t, unsigned bytes)
+{
+    return reinterpret_cast<const E*>(static_cast<const char*>(base) + (unsigned long long)t * bytes);
+}
+template <typename E>
+__device__ __forceinline__ E* row(void* base, unsigned t, unsigned bytes)
+{
+    return reinterpret_cast<E*>(static_cast<char*>(base) + (unsigned long long)t * bytes);
+}
+
+// Two channels, or four states of B or C, as loaded.
+template <typename T> struct Raw;
+template <> struct Raw<float> { typedef float2 pair; typedef float4 quad; };
+template <> struct Raw<__nv_bfloat16> { typedef unsigned pair; typedef uint2 quad; };
+__device__ __forceinline__ float2 widen(float2 v) { return v; }
+__device__ __forceinline__ float2 widen(unsigned v)
+{
+    float2 r;
+    unpack2(v, r.x, r.y);
+    return r;
+}
+
+// 2 P consecutive elements in shared memory, in pairs.  bf16 stays bf16 there: the
+// walk is bound by the words that shared memory returns, and widening is cheap.
+template <int P>
+__device__ __forceinline__ void read_states(const __nv_bfloat16* p, f32x2 (&v)[P])
+{
+#pragma unroll
+    for (int i = 0; i < P; i += 2) {
+        const uint2 t = *reinterpret_cast<const uint2*>(p + 2 * i);
+        v[i] = pack(__uint_as_float(t.x << 16), __uint_as_float(t.x & 0xffff0000u));
+        v[i + 1] = pack(__uint_as_float(t.y << 16), __uint_as_float(t.y & 0xffff0000u));
+    }
+}
+template <int P>
+__device__ __forceinline__ void read_states(const float* p, f32x2 (&v)[P])
+{
+#pragma unroll
+    for (int i = 0; i < P; i += 2) {
+        const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(p + 2 * i);
+        v[i] = t.x;
+        v[i + 1] = t.y;
+    }
+}
+template <int P>
+__device__ __forceinline__ void write_states(float* p, const f32x2 (&v)[P])
+{
+#pragma unroll
+    for (int i = 0; i < P; i += 2) *reinterpret_cast<ulonglong2*>(p + 2 * i) = make_ulonglong2(v[i], v[i + 1]);
+}
+
+// The recurrence is a chain of one multiply-add per token and state; everything
+// else of a token is independent of it.  So the warps of a block take turns along
+// the sequence: each computes the step sizes, decays and inputs of its TK tokens
+// into registers, waits for the state of the warp before it, runs the chain (TK
+// multiply-adds), hands the state on, and only then forms y, the gate and the
+// output.  Every exponential is computed once, W warps per 8 channels are at work
+// at any time, and the warps meet nowhere but at that hand-over (a named barrier
+// of the two warps).
+template <typename T, int N, int CK>
+__global__ void __launch_bounds__(Walk<N>::THREADS, 4)
+ssm_walk_kernel(const SsmDev p, const WalkBwd wb)
+{
+    using K = Walk<N>;
+    constexpr int TK = K::TK, DT = K::DT, L = K::L, W = K::W, NPT = K::NPT, R = K::R, VP = K::VP;
+    __shared__ __align__(16) float2 sDU[W][TK * K::DUROW];   // [token][channel]: Delta, u
+    __shared__ __align__(16) T sB[W][TK * N], sC[W][TK * N];  // [token][N]
+    __shared__ float4 sState[W][DT * N / 4];                 // handed on by warp w: [lane][NPT]
+    __shared__ __align__(16) float sY[W][TK * K::YROW];
 
     if (CK == 0) flag_bad_sequences(p.q);
     const int ntiles = p.tiles * p.G;
     const int tile = blockIdx.x % ntiles, seq = blockIdx.x / ntiles;
-    const int Dg = p.D / p.G, g = tile / p.tiles, off = (tile % p.tiles) * DT;
-    const int c0 = g * Dg + off, nvalid = min(DT, Dg - off);
-    const int tid = threadIdx.x, l = tid % L, c = tid / L;
-    const bool live = c < nvalid;
+    const int Dg = p.D / p.G, g = tile / p.tiles, c0 = g * Dg + tile % p.tiles * DT;   // D / G is a multiple of 8
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = lane / L, l = lane % L;
 
-    long long s = p.q.begin(seq), e = p.q.begin(seq + 1);
+    const long long s = p.q.begin(seq);
+    long long e = p.q.begin(seq + 1);
     if (e < s || !Seqs::inside(s, e, p.q.tokens)) e = s;
+    const int len = (int)(e - s);
 
-    const T* x = static_cast<const T*>(p.x) + c0;
-    const T* dt = static_cast<const T*>(p.dt) + c0;
-    const T* z = p.z ? static_cast<const T*>(p.z) + c0 : nullptr;
-    const T* b = static_cast<const T*>(p.b) + g * N;
-    const T* cc = static_cast<const T*>(p.c) + g * N;
-
-    float A2[NPT], h[NPT];
+    f32x2 A2[NPT / 2], h[NPT / 2];
     const long long srow = ((long long)seq * p.D + c0 + c) * N + l * NPT;
 #pragma unroll
-    for (int n = 0; n < NPT; ++n) {
-        A2[n] = live ? p.A[(long long)(c0 + c) * N + l * NPT + n] * kLog2e : 0.f;
-        h[n] = live && p.s0 ? p.s0[srow + n] : 0.f;
+    for (int n = 0; n < NPT / 2; ++n) {
+        const float2 a = *reinterpret_cast<const float2*>(p.A + (long long)(c0 + c) * N + l * NPT + 2 * n);
+        A2[n] = pack(a.x * kLog2e, a.y * kLog2e);
+        h[n] = p.s0 ? *reinterpret_cast<const f32x2*>(p.s0 + srow + 2 * n) : 0ull;
     }
-    // the thread's EP elements outside the walk: token rt, channels rc ..
-    const int rt = tid * EP / DT, rc = tid * EP % DT;
-    const bool rlive = rc < nvalid;
-    float bias[EP], skip[EP];
-#pragma unroll
-    for (int k = 0; k < EP; ++k) {
-        bias[k] = rlive && p.dt_bias ? p.dt_bias[c0 + rc + k] : 0.f;
-        skip[k] = rlive && p.skip ? p.skip[c0 + rc + k] : 0.f;
-    }
+    const bool gated = p.z != nullptr;
 
-    auto fetch = [&](long long t0, int stage) {
-        T* st = reinterpret_cast<T*>(smem + stage * K::STAGE);
-        fetch_rows<T, TT, DT, 128>(st, x, p.ldx, t0, e, nvalid);
-        fetch_rows<T, TT, DT, 128>(st + TT * DT, dt, p.lddt, t0, e, nvalid);
-        if (z) fetch_rows<T, TT, DT, 128>(st + 2 * TT * DT, z, p.ldz, t0, e, nvalid);
-        fetch_rows<T, TT, N, 128>(st + 3 * TT * DT, b, p.ldb, t0, e, N);
-        fetch_rows<T, TT, N, 128>(st + 3 * TT * DT + TT * N, cc, p.ldc, t0, e, N);
+    // the lane's elements outside the chain: channels ec, ec + 1 of token et, and a
+    // quad each of B and C
+    const bool mine = lane < TK * DT / 2;
+    const int et = lane / (DT / 2), ec = c0 + lane % (DT / 2) * 2, bt = lane / (N / 4), bn = g * N + lane % (N / 4) * 4;
+    float2 bias = make_float2(0.f, 0.f), skip = bias;
+    if (p.dt_bias) bias = *reinterpret_cast<const float2*>(p.dt_bias + ec);
+    if (p.skip) skip = *reinterpret_cast<const float2*>(p.skip + ec);
+    const int first = (int)s;
+
+    typedef typename Raw<T>::pair Pair;
+    typedef typename Raw<T>::quad Quad;
+    Pair nx, ndt, nz;
+    float2 ngy;
+    Quad nb, nc;
+    auto fetch = [&](int t0) {   // the lane's inputs of the TK tokens from t0 on; zero behind the end
+        nx = ndt = nz = Pair{};
+        nb = nc = Quad{};
+        if (mine && t0 + et < len) {
+            const unsigned t = first + t0 + et;
+            nx = *reinterpret_cast<const Pair*>(row<T>(p.x, t, p.ldx) + ec);
+            ndt = *reinterpret_cast<const Pair*>(row<T>(p.dt, t, p.lddt) + ec);
+            if (gated) nz = *reinterpret_cast<const Pair*>(row<T>(p.z, t, p.ldz) + ec);
+            if (CK > 0) ngy = *reinterpret_cast<const float2*>(row<float>(wb.gy, t, 4u * p.D) + ec);
+        }
+        if (t0 + bt < len) {
+            const unsigned t = first + t0 + bt;
+            nb = *reinterpret_cast<const Quad*>(row<T>(p.b, t, p.ldb) + bn);
+            nc = *reinterpret_cast<const Quad*>(row<T>(p.c, t, p.ldc) + bn);
+        }
     };
-    int stage = 0;
-    if (s < e) fetch(s, 0);
-    cp_async_commit();
-    for (long long t0 = s; t0 < e; t0 += TT, stage ^= 1) {
-        if (t0 + TT < e) fetch(t0 + TT, stage ^ 1);
-        cp_async_commit();
-        cp_async_wait<1>();
-        __syncthreads();
-        const T* st = reinterpret_cast<const T*>(smem + stage * K::STAGE);
-        const bool rin = t0 + rt < e;
-        float xv[EP];
-        load_vec<EP>(st + rt * DT + rc, xv);
-        {
-            float dv[EP];
-            load_vec<EP>(st + TT * DT + rt * DT + rc, dv);
-#pragma unroll
-            for (int k = 0; k < EP; ++k) {
-                const float v = dv[k] + bias[k];
-                const float delta = !rin || !rlive ? 0.f : p.softplus ? softplus(v) : v;
-                *reinterpret_cast<float2*>(sDU + rt * K::DUROW + 2 * (rc + k)) = make_float2(delta, delta * xv[k]);
-            }
-        }
-        for (int i = tid * 2; i < TT * N; i += 256) {
-            float v[2];
-            load_vec<2>(st + 3 * TT * DT + i, v);
-            store_vec<2>(sB + i, v);
-            load_vec<2>(st + 3 * TT * DT + TT * N + i, v);
-            store_vec<2>(sC + i, v);
-        }
-        __syncthreads();
+    fetch(w * TK);
 
-        const int steps = (int)min((long long)TT, e - t0);
-        for (int tb = 0; tb < steps; tb += L) {
-            float acc[L];
-#pragma unroll
-            for (int j = 0; j < L; ++j) {
-                const int t = tb + j;
-                if constexpr (CK > 0) {
-                    if (j % (CK < L ? CK : L) == 0 && t % CK == 0 && t < steps && live) {
-                        float* o = w.ckpt + (ckpt_base<CK>(p.q, seq, s) + (t0 - s + t) / CK) * ((long long)p.D * N) +
-                                   (long long)(c0 + c) * N + l * NPT;
-#pragma unroll
-                        for (int n = 0; n < NPT; ++n) o[n] = h[n];
-                    }
-                }
-                const float2 du = *reinterpret_cast<const float2*>(sDU + t * K::DUROW + 2 * c);
-                acc[j] = 0.f;
-#pragma unroll
-                for (int n = 0; n < NPT; ++n) {
-                    const float a = exp2_approx(du.x * A2[n]);
-                    h[n] = fmaf(a, h[n], du.y * sB[t * N + l * NPT + n]);
-                    acc[j] = fmaf(sC[t * N + l * NPT + n], h[n], acc[j]);
-                }
-            }
-            reduce_transposed<L, L, 1>(acc, tid);
-            __syncwarp();
-            // every lane of the group has read its (Delta, u) of these L tokens
-            sDU[(tb + l) * K::DUROW + 2 * c] = acc[0];
+    for (int t0 = w * TK; t0 < len; t0 += W * TK) {
+        const float2 x = widen(nx), z = widen(nz), gy = ngy;
+        __syncwarp();
+        if (mine) {
+            const float2 dt = widen(ndt);
+            f32x2 d = add2(pack(dt.x, dt.y), pack(bias.x, bias.y));
+            float d0, d1, u0, u1;
+            unpack(d, d0, d1);
+            if (p.softplus) unpack(softplus2(d0, d1), d0, d1);
+            if (t0 + et >= len) d0 = d1 = 0.f;   // a token behind the end leaves the state as it is
+            unpack(mul2(pack(d0, d1), pack(x.x, x.y)), u0, u1);
+            *reinterpret_cast<float4*>(&sDU[w][et * K::DUROW + ec - c0]) = make_float4(d0, u0, d1, u1);
         }
-        __syncthreads();
-        if (CK > 0) {
-            if (z && rin && rlive) {
-                float zv[EP], g[EP];
-                const long long o = (t0 + rt) * p.D + c0 + rc;
-                load_vec<EP>(st + 2 * TT * DT + rt * DT + rc, zv);
-                load_vec<EP>(w.gy + o, g);
+        reinterpret_cast<Quad*>(sB[w])[lane] = nb;
+        reinterpret_cast<Quad*>(sC[w])[lane] = nc;
+        __syncwarp();
+        fetch(t0 + W * TK);
+
+        f32x2 a[TK][NPT / 2], b[TK][NPT / 2];
+        const T* pB = sB[w] + l * NPT;
 #pragma unroll
-                for (int k = 0; k < EP; ++k)
-                    g[k] *= fmaf(skip[k], xv[k], sDU[rt * K::DUROW + 2 * (rc + k)]) * silu_grad(zv[k]);
-                store_vec<EP>(w.gz + o, g);
+        for (int j = 0; j < TK; ++j) {
+            const float2 d = sDU[w][j * K::DUROW + c];
+            const f32x2 dd = pack(d.x, d.x), uu = pack(d.y, d.y);
+            f32x2 B[NPT / 2];
+            read_states(pB + j * N, B);
+#pragma unroll
+            for (int n = 0; n < NPT / 2; ++n) {
+                a[j][n] = decay2(dd, A2[n]);
+                b[j][n] = mul2(uu, B[n]);
             }
-        } else if (rin && rlive) {
-            float out[EP];
-#pragma unroll
-            for (int k = 0; k < EP; ++k) out[k] = fmaf(skip[k], xv[k], sDU[rt * K::DUROW + 2 * (rc + k)]);
-            if (z) {
-                float zv[EP];
-                load_vec<EP>(st + 2 * TT * DT + rt * DT + rc, zv);
-#pragma unroll
-                for (int k = 0; k < EP; ++k) out[k] *= silu(zv[k]);
-            }
-            const long long o = (t0 + rt) * p.D + c0 + rc;
-            if (p.o_bf16)
-                store_vec<EP>(static_cast<__nv_bfloat16*>(p.y) + o, out);
-            else
-                store_vec<EP>(static_cast<float*>(p.y) + o, out);
         }
-        __syncthreads();   // the stage and (Delta, u) are free
+        if (t0 > 0) {
+            const int from = (w + W - 1) % W;
+            bar_sync(1 + from, 64);
+            read_states(reinterpret_cast<const float*>(sState[from]) + lane * NPT, h);
+        }
+        if constexpr (CK > 0) {
+            if (t0 % CK == 0) {
+                float* o = wb.ckpt + ((ckpt_base<CK>(p.q, seq, s) + t0 / CK) * p.D + c0 + c) * N + l * NPT;
+#pragma unroll
+                for (int n = 0; n < NPT / 2; ++n) *reinterpret_cast<f32x2*>(o + 2 * n) = h[n];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < TK; ++j)
+#pragma unroll
+            for (int n = 0; n < NPT / 2; ++n) b[j][n] = h[n] = fma2(a[j][n], h[n], b[j][n]);   // b: now the states
+        if (t0 + TK < len) {
+            write_states(reinterpret_cast<float*>(sState[w]) + lane * NPT, h);
+            bar_arrive(1 + w, 64);
+        } else if (CK == 0 && p.sT) {
+#pragma unroll
+            for (int n = 0; n < NPT / 2; ++n) *reinterpret_cast<f32x2*>(p.sT + srow + 2 * n) = h[n];
+        }
+        float y[TK];
+        const T* pC = sC[w] + l * NPT;
+#pragma unroll
+        for (int j = 0; j < TK; ++j) {
+            f32x2 C[NPT / 2], sum;
+            read_states(pC + j * N, C);
+            sum = mul2(C[0], b[j][0]);
+#pragma unroll
+            for (int n = 1; n < NPT / 2; ++n) sum = fma2(C[n], b[j][n], sum);
+            float lo, hi;
+            unpack(sum, lo, hi);
+            y[j] = lo + hi;
+        }
+        reduce_transposed<TK, R, L / R>(y, lane);
+#pragma unroll
+        for (int v = 0; v < VP; ++v) {
+#pragma unroll
+            for (int m = L / R / 2; m >= 1; m >>= 1) y[v] += __shfl_xor_sync(0xffffffffu, y[v], m);
+            if (l % (L / R) == 0) sY[w][(l / (L / R) * VP + v) * K::YROW + c] = y[v];
+        }
+        __syncwarp();
+        if (mine && t0 + et < len && (CK == 0 || gated)) {
+            const float2 r = *reinterpret_cast<const float2*>(&sY[w][et * K::YROW + ec - c0]);
+            f32x2 out = fma2(pack(skip.x, skip.y), pack(x.x, x.y), pack(r.x, r.y));
+            float o[2];
+            const unsigned t = first + t0 + et;
+            if constexpr (CK > 0) {
+                unpack(out, o[0], o[1]);
+                o[0] *= gy.x * silu_grad(z.x);
+                o[1] *= gy.y * silu_grad(z.y);
+                store_vec<2>(row<float>(wb.gz, t, 4u * p.D) + ec, o);
+            } else {
+                if (gated) out = mul2(out, silu2(z.x, z.y));
+                unpack(out, o[0], o[1]);
+                if (p.o_bf16)
+                    store_vec<2>(row<__nv_bfloat16>(p.y, t, 2u * p.D) + ec, o);
+                else
+                    store_vec<2>(row<float>(p.y, t, 4u * p.D) + ec, o);
+            }
+        }
     }
-    if (CK == 0 && p.sT && live) {
+    if (CK == 0 && p.sT && len == 0 && w == 0) {
 #pragma unroll
-        for (int n = 0; n < NPT; ++n) p.sT[srow + n] = h[n];
+        for (int n = 0; n < NPT / 2; ++n) *reinterpret_cast<f32x2*>(p.sT + srow + 2 * n) = h[n];
     }
 }
 
@@ -182,29 +282,30 @@ ssm_step_kernel(const SsmDev p, int n_seq, int RN)
     if (d >= p.D) return;   // D is a multiple of 8: whole groups of L <= 16 lanes leave together
     const unsigned mask = __activemask();
     const int g = d / (p.D / p.G);
-    const float4 A = *reinterpret_cast<const float4*>(p.A + (long long)d * N + 4 * l);
+    float4 A = *reinterpret_cast<const float4*>(p.A + (long long)d * N + 4 * l);
+    A.x *= kLog2e; A.y *= kLog2e; A.z *= kLog2e; A.w *= kLog2e;
     const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.skip ? p.skip[d] : 0.f;
     const int i1 = min((int)(blockIdx.y + 1) * RN, n_seq);
     for (int i = blockIdx.y * RN; i < i1; ++i) {
         float4* sp = reinterpret_cast<float4*>(p.sT + ((long long)i * p.D + d) * N + 4 * l);
         float4 h = *sp;
-        const float x = Elem<T>::load(static_cast<const T*>(p.x) + i * p.ldx + d);
-        const float v = Elem<T>::load(static_cast<const T*>(p.dt) + i * p.lddt + d) + bias;
+        const float x = Elem<T>::load(row<T>(p.x, i, p.ldx) + d);
+        const float v = Elem<T>::load(row<T>(p.dt, i, p.lddt) + d) + bias;
         float b[4], c[4];
-        load_vec<4>(static_cast<const T*>(p.b) + i * p.ldb + g * N + 4 * l, b);
-        load_vec<4>(static_cast<const T*>(p.c) + i * p.ldc + g * N + 4 * l, c);
-        const float delta = p.softplus ? softplus(v) : v, u = delta * x, d2 = delta * kLog2e;
-        h.x = fmaf(exp2_approx(d2 * A.x), h.x, u * b[0]);
-        h.y = fmaf(exp2_approx(d2 * A.y), h.y, u * b[1]);
-        h.z = fmaf(exp2_approx(d2 * A.z), h.z, u * b[2]);
-        h.w = fmaf(exp2_approx(d2 * A.w), h.w, u * b[3]);
+        load_vec<4>(row<T>(p.b, i, p.ldb) + g * N + 4 * l, b);
+        load_vec<4>(row<T>(p.c, i, p.ldc) + g * N + 4 * l, c);
+        const float delta = p.softplus ? softplus(v) : v, u = delta * x;
+        h.x = fmaf(exp2_approx(fmaf(delta, A.x, kDecayShift)), h.x, u * b[0]);
+        h.y = fmaf(exp2_approx(fmaf(delta, A.y, kDecayShift)), h.y, u * b[1]);
+        h.z = fmaf(exp2_approx(fmaf(delta, A.z, kDecayShift)), h.z, u * b[2]);
+        h.w = fmaf(exp2_approx(fmaf(delta, A.w, kDecayShift)), h.w, u * b[3]);
         *sp = h;
         float y = fmaf(c[0], h.x, c[1] * h.y) + fmaf(c[2], h.z, c[3] * h.w);
 #pragma unroll
         for (int m = L / 2; m >= 1; m >>= 1) y += __shfl_xor_sync(mask, y, m);
         if (l == 0) {
             y = fmaf(skip, x, y);
-            if (p.z) y *= silu(Elem<T>::load(static_cast<const T*>(p.z) + i * p.ldz + d));
+            if (p.z) y *= silu(Elem<T>::load(row<T>(p.z, i, p.ldz) + d));
             const long long o = (long long)i * p.D + d;
             if (p.o_bf16)
                 static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(y);
@@ -218,7 +319,9 @@ static SsmDev ssm_dev(const SsmArgs& a, void* y, float* sT, kda_dtype o_dtype)
 {
     SsmDev p;
     p.x = a.x; p.dt = a.dt; p.b = a.b; p.c = a.c; p.z = a.z;
-    p.ldx = a.ldx; p.lddt = a.lddt; p.ldb = a.ldb; p.ldc = a.ldc; p.ldz = a.ldz;
+    const unsigned es = a.dtype == KDA_BF16 ? 2 : 4;   // strides in bytes: below 2^32
+    p.ldx = (unsigned)a.ldx * es; p.lddt = (unsigned)a.lddt * es; p.ldb = (unsigned)a.ldb * es;
+    p.ldc = (unsigned)a.ldc * es; p.ldz = (unsigned)a.ldz * es;
     p.A = a.A; p.skip = a.skip; p.dt_bias = a.dt_bias; p.s0 = a.s0;
     p.y = y; p.sT = sT;
     p.q = Seqs{a.cu, a.nseq, a.T, a.tokens};
@@ -227,34 +330,23 @@ static SsmDev ssm_dev(const SsmArgs& a, void* y, float* sT, kda_dtype o_dtype)
     return p;
 }
 
-template <typename T, int N, int L, int CK = 0>
+template <typename T, int N, int CK = 0>
 static cudaError_t launch_walk(const SsmArgs& a, SsmDev p, cudaStream_t s, const WalkBwd& w = WalkBwd{})
 {
-    using K = Walk<T, N, L>;
-    p.tiles = (a.D / a.G + K::DT - 1) / K::DT;
+    using K = Walk<N>;
+    p.tiles = a.D / a.G / K::DT;
     const long long blocks = (long long)a.nseq * p.tiles * a.G;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = cudaFuncSetAttribute(
-        ssm_walk_kernel<T, N, L, CK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM);
-    if (e != cudaSuccess) return e;
-    ssm_walk_kernel<T, N, L, CK><<<(unsigned)blocks, K::THREADS, K::SMEM, s>>>(p, w);
+    ssm_walk_kernel<T, N, CK><<<(unsigned)blocks, K::THREADS, 0, s>>>(p, w);
     return cudaGetLastError();
 }
 
 template <typename T>
 static cudaError_t walk_dispatch(const SsmArgs& a, const SsmDev& p, cudaStream_t s)
 {
-    // States per lane: 4 where that still gives every scheduler of the 148 SMs
-    // about two warps, else fewer (more lanes per channel).
-    const long long warps = (long long)a.nseq * a.D * (a.N / 4) / 32;
-    const bool wide = warps >= 148LL * 8;
-    if (a.N == 16) {
-        if (wide) return launch_walk<T, 16, 4>(a, p, s);
-        if (warps >= 148LL * 2) return launch_walk<T, 16, 8>(a, p, s);
-        return launch_walk<T, 16, 16>(a, p, s);
-    }
-    if (a.N == 32) return wide ? launch_walk<T, 32, 8>(a, p, s) : launch_walk<T, 32, 16>(a, p, s);
-    return launch_walk<T, 64, 16>(a, p, s);
+    if (a.N == 16) return launch_walk<T, 16>(a, p, s);
+    if (a.N == 32) return launch_walk<T, 32>(a, p, s);
+    return launch_walk<T, 64>(a, p, s);
 }
 
 template <typename T>

@@ -19,8 +19,88 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(K) : "memory");
 }
 
-// softplus(v) = max(v, 0) + log(1 + e^-|v|), to fp32 accuracy for every v.
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+// Two fp32 values in one 64-bit register: the packed multiply-add does both in
+// one issue slot.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack(float a, float b)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(f32x2 v, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 silu2(float x, float y)
+{
+    const f32x2 v = pack(x, y);
+    float a, b;
+    unpack(mul2(v, pack(-kLog2e, -kLog2e)), a, b);
+    unpack(add2(pack(exp2_approx(a), exp2_approx(b)), pack(1.f, 1.f)), a, b);
+    return mul2(v, pack(rcp_approx(a), rcp_approx(b)));
+}
+
+// softplus(v) = max(v, 0) + log(1 + e), e = e^-|v|, of two values, to fp32 accuracy
+// for every v.  e: 2^(-|v| log2 e) with the rounding error of the exponent put back
+// (log2 e in two parts).  log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, without
+// the cancellation of 1 + e; atanh(s) / s is a degree-4 polynomial in s^2 (largest
+// relative error 4e-9, fitted by reweighted least squares).
+__device__ __forceinline__ f32x2 softplus2(float v0, float v1)
+{
+    auto two = [](float x) { return pack(x, x); };
+    const f32x2 t = pack(-fabsf(v0), -fabsf(v1));
+    const f32x2 nhi = mul2(t, two(-kLog2e));
+    const f32x2 lo = fma2(t, two(1.9259629e-8f), fma2(t, two(kLog2e), nhi));
+    float h0, h1;
+    unpack(nhi, h0, h1);
+    f32x2 e = pack(exp2_approx(-h0), exp2_approx(-h1));
+    e = fma2(mul2(e, lo), two(0.69314718f), e);
+    unpack(fma2(e, two(1.f), two(2.f)), h0, h1);
+    const f32x2 s = mul2(e, pack(rcp_approx(h0), rcp_approx(h1))), q = mul2(s, s);
+    f32x2 p = fma2(q, two(0.14089163f), two(0.13980302f));
+    p = fma2(q, p, two(0.20012455f));
+    p = fma2(q, p, two(0.33333158f));
+    p = fma2(q, p, two(1.f));
+    return fma2(mul2(s, two(2.f)), p, pack(fmaxf(v0, 0.f), fmaxf(v1, 0.f)));
+}
+__device__ __forceinline__ float softplus(float v)
+{
+    float r, unused;
+    unpack(softplus2(v, v), r, unused);
+    return r;
+}
+
+// Decays 2^(Delta A2) of two states.  ex2.approx is below the true value by 0.4
+// 2^-24 on average for exponents in [-0.25, -0.003] (measured), which hundreds of
+// slow decays in a row would add up; the exponent is moved by that much, at no
+// cost in the multiply.
+constexpr float kDecayShift = 3.4e-8f;   // 0.4 2^-24 log2 e
+__device__ __forceinline__ f32x2 decay2(f32x2 delta, f32x2 A2)
+{
+    float x, y;
+    unpack(fma2(delta, A2, pack(kDecayShift, kDecayShift)), x, y);
+    return pack(exp2_approx(x), exp2_approx(y));
+}
 
 // Sums p[j] over LANES lanes that lie STRIDE apart, for V >= LANES values at
 // once: the lane with index i = (lane / STRIDE) % LANES gets the sums of values
@@ -52,27 +132,13 @@ __device__ __forceinline__ long long ckpt_base(const Seqs& q, int seq, long long
 
 struct SsmDev {
     const void *x, *dt, *b, *c, *z;
-    long long ldx, lddt, ldb, ldc, ldz;
+    unsigned ldx, lddt, ldb, ldc, ldz;   // bytes from row to row
     const float *A, *skip, *dt_bias, *s0;
     void* y;
     float* sT;
     Seqs q;
     int D, G, tiles;   // tiles: channel tiles per group
     bool softplus, o_bf16;
-};
-
-// Shape of a walk: 128 threads; a channel's N states lie on L lanes (NPT states
-// each), so a block owns DT = 128 / L channels and walks its sequence in tiles
-// of TT tokens.
-template <typename T, int N_, int L_>
-struct Walk {
-    static constexpr int N = N_, L = L_, NPT = N / L, THREADS = 128, DT = THREADS / L;
-    static constexpr int TT = L == 4 ? 32 : N == 64 ? 32 : 64;
-    static constexpr int EP = TT * DT / THREADS;          // elements per thread outside the walk
-    static constexpr int DUROW = 2 * DT + 16;             // floats per token of (Delta, u); rows 16 banks apart
-    static constexpr size_t RAW_X = (size_t)TT * DT * sizeof(T), RAW_B = (size_t)TT * N * sizeof(T);
-    static constexpr size_t STAGE = 3 * RAW_X + 2 * RAW_B;
-    static constexpr size_t SMEM = 2 * STAGE + (size_t)TT * DUROW * 4 + 2 * (size_t)TT * N * 4;
 };
 
 // One tile of rows [t0, t0 + TT) of a token-major array into shared memory, 16

@@ -88,11 +88,11 @@ ssm_reverse_kernel(const BwdDev b)
         if (e < s || !Seqs::inside(s, e, p.q.tokens)) e = s;
         auto fetch = [&](long long t0, int stage) {
             T* st = reinterpret_cast<T*>(smem + stage * K::STAGE);
-            fetch_rows<T, TT, DT, NT>(st, x, p.ldx, t0, e, nvalid);
-            fetch_rows<T, TT, DT, NT>(st + TT * DT, dt, p.lddt, t0, e, nvalid);
-            if (z) fetch_rows<T, TT, DT, NT>(st + 2 * TT * DT, z, p.ldz, t0, e, nvalid);
-            fetch_rows<T, TT, N, NT>(st + 3 * TT * DT, bb, p.ldb, t0, e, N);
-            fetch_rows<T, TT, N, NT>(st + 3 * TT * DT + TT * N, cc, p.ldc, t0, e, N);
+            fetch_rows<T, TT, DT, NT>(st, x, p.ldx / sizeof(T), t0, e, nvalid);
+            fetch_rows<T, TT, DT, NT>(st + TT * DT, dt, p.lddt / sizeof(T), t0, e, nvalid);
+            if (z) fetch_rows<T, TT, DT, NT>(st + 2 * TT * DT, z, p.ldz / sizeof(T), t0, e, nvalid);
+            fetch_rows<T, TT, N, NT>(st + 3 * TT * DT, bb, p.ldb / sizeof(T), t0, e, N);
+            fetch_rows<T, TT, N, NT>(st + 3 * TT * DT + TT * N, cc, p.ldc / sizeof(T), t0, e, N);
             fetch_rows<float, TT, DT, NT>(reinterpret_cast<float*>(st + 3 * TT * DT + 2 * TT * N), b.gy + c0, p.D, t0, e,
                                           nvalid);
         };
@@ -148,8 +148,7 @@ ssm_reverse_kernel(const BwdDev b)
 
             for (int tb = (int)(min((long long)TT, e - t0) - 1) / CK * CK; tb >= 0; tb -= CK) {
                 float h0[NPT], a[CK][NPT], h[CK][NPT];
-                const float* cp = b.ckpt + (ckpt_base<CK>(p.q, seq, s) + (t0 - s + tb) / CK) * ((long long)p.D * N) +
-                                  (long long)(c0 + c) * N + l * NPT;
+                const float* cp = b.ckpt + ((ckpt_base<CK>(p.q, seq, s) + (t0 - s + tb) / CK) * p.D + c0 + c) * N + l * NPT;
 #pragma unroll
                 for (int n = 0; n < NPT; ++n) h0[n] = live ? cp[n] : 0.f;
 #pragma unroll
@@ -157,7 +156,7 @@ ssm_reverse_kernel(const BwdDev b)
                     const float2 du = *reinterpret_cast<const float2*>(sDU + (tb + j) * K::DUROW + 2 * c);
 #pragma unroll
                     for (int n = 0; n < NPT; ++n) {
-                        a[j][n] = exp2_approx(du.x * (A[n] * kLog2e));
+                        a[j][n] = exp2_approx(fmaf(du.x, A[n] * kLog2e, kDecayShift));
                         h[j][n] = fmaf(a[j][n], j ? h[j - 1][n] : h0[n], du.y * sB[(tb + j) * N + l * NPT + n]);
                     }
                 }
@@ -312,7 +311,7 @@ static int bwd_slots(int nseq, int ntiles)
 
 template <int N>
 struct BwdShape {
-    static constexpr int L = N == 64 ? 16 : 8, CK = N == 16 ? 16 : 8, DT = 16;
+    static constexpr int L = N == 64 ? 16 : 8, CK = 8, DT = 16;
 };
 
 struct BwdWorkspace {
@@ -353,7 +352,7 @@ static cudaError_t launch_bwd(const SsmArgs& a, const SsmGrads& g, void* ws, cud
     b.partv = reinterpret_cast<float*>(base + w.partv);
     b.p.tiles = (a.D / a.G + S::DT - 1) / S::DT;
     b.slots = bwd_slots(a.nseq, b.p.tiles * a.G);
-    cudaError_t e = launch_walk<T, N, N / 4, S::CK>(a, b.p, s,
+    cudaError_t e = launch_walk<T, N, S::CK>(a, b.p, s,
                                                     WalkBwd{g.gy, g.gz, reinterpret_cast<float*>(base + w.ckpt)});
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(ssm_reverse_kernel<T, N, S::L, S::CK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
