@@ -41,60 +41,6 @@ __device__ __forceinline__ void bar_arrive(int id, int threads)
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Row t of an array with rows `bytes` apart: one wide multiply-add, and no pointer
-// is kept in registers.
-template <typename E>
-__device__ __forceinline__ const E* row(const void* base, unsigned t, unsigned bytes)
-{
-    return reinterpret_cast<const E*>(static_cast<const char*>(base) + (unsigned long long)t * bytes);
-}
-template <typename E>
-__device__ __forceinline__ E* row(void* base, unsigned t, unsigned bytes)
-{
-    return reinterpret_cast<E*>(static_cast<char*>(base) + (unsigned long long)t * bytes);
-}
-
-// Two channels, or four states of B or C, as loaded.
-template <typename T> struct Raw;
-template <> struct Raw<float> { typedef float2 pair; typedef float4 quad; };
-template <> struct Raw<__nv_bfloat16> { typedef unsigned pair; typedef uint2 quad; };
-__device__ __forceinline__ float2 widen(float2 v) { return v; }
-__device__ __forceinline__ float2 widen(unsigned v)
-{
-    float2 r;
-    unpack2(v, r.x, r.y);
-    return r;
-}
-
-// 2 P consecutive elements in shared memory, in pairs.  bf16 stays bf16 there: the
-// walk is bound by the words that shared memory returns, and widening is cheap.
-template <int P>
-__device__ __forceinline__ void read_states(const __nv_bfloat16* p, f32x2 (&v)[P])
-{
-#pragma unroll
-    for (int i = 0; i < P; i += 2) {
-        const uint2 t = *reinterpret_cast<const uint2*>(p + 2 * i);
-        v[i] = pack(__uint_as_float(t.x << 16), __uint_as_float(t.x & 0xffff0000u));
-        v[i + 1] = pack(__uint_as_float(t.y << 16), __uint_as_float(t.y & 0xffff0000u));
-    }
-}
-template <int P>
-__device__ __forceinline__ void read_states(const float* p, f32x2 (&v)[P])
-{
-#pragma unroll
-    for (int i = 0; i < P; i += 2) {
-        const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(p + 2 * i);
-        v[i] = t.x;
-        v[i + 1] = t.y;
-    }
-}
-template <int P>
-__device__ __forceinline__ void write_states(float* p, const f32x2 (&v)[P])
-{
-#pragma unroll
-    for (int i = 0; i < P; i += 2) *reinterpret_cast<ulonglong2*>(p + 2 * i) = make_ulonglong2(v[i], v[i + 1]);
-}
-
 // The recurrence is a chain of one multiply-add per token and state; everything
 // else of a token is independent of it.  So the warps of a block take turns along
 // the sequence: each computes the step sizes, decays and inputs of its TK tokens

@@ -6,19 +6,6 @@
 namespace kda {
 namespace mixer {
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid)
-{
-    const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
-    const int bytes = valid ? 16 : 0;   // 0: the 16 bytes are zero-filled and src is not read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int K>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(K) : "memory");
-}
-
 // Two fp32 values in one 64-bit register: the packed multiply-add does both in
 // one issue slot.
 typedef unsigned long long f32x2;
@@ -130,6 +117,60 @@ __device__ __forceinline__ long long ckpt_base(const Seqs& q, int seq, long long
     return q.cu ? begin / CK + seq : (long long)seq * ((q.T + CK - 1) / CK);
 }
 
+// Row t of an array with rows `bytes` apart: one wide multiply-add, and no pointer
+// is kept in registers.
+template <typename E>
+__device__ __forceinline__ const E* row(const void* base, unsigned t, unsigned bytes)
+{
+    return reinterpret_cast<const E*>(static_cast<const char*>(base) + (unsigned long long)t * bytes);
+}
+template <typename E>
+__device__ __forceinline__ E* row(void* base, unsigned t, unsigned bytes)
+{
+    return reinterpret_cast<E*>(static_cast<char*>(base) + (unsigned long long)t * bytes);
+}
+
+// Two channels, or four states of B or C, as loaded.
+template <typename T> struct Raw;
+template <> struct Raw<float> { typedef float2 pair; typedef float4 quad; };
+template <> struct Raw<__nv_bfloat16> { typedef unsigned pair; typedef uint2 quad; };
+__device__ __forceinline__ float2 widen(float2 v) { return v; }
+__device__ __forceinline__ float2 widen(unsigned v)
+{
+    float2 r;
+    unpack2(v, r.x, r.y);
+    return r;
+}
+
+// 2 P consecutive elements in shared memory, in pairs.  bf16 stays bf16 there: the
+// walk is bound by the words that shared memory returns, and widening is cheap.
+template <int P>
+__device__ __forceinline__ void read_states(const __nv_bfloat16* p, f32x2 (&v)[P])
+{
+#pragma unroll
+    for (int i = 0; i < P; i += 2) {
+        const uint2 t = *reinterpret_cast<const uint2*>(p + 2 * i);
+        v[i] = pack(__uint_as_float(t.x << 16), __uint_as_float(t.x & 0xffff0000u));
+        v[i + 1] = pack(__uint_as_float(t.y << 16), __uint_as_float(t.y & 0xffff0000u));
+    }
+}
+template <int P>
+__device__ __forceinline__ void read_states(const float* p, f32x2 (&v)[P])
+{
+#pragma unroll
+    for (int i = 0; i < P; i += 2) {
+        const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(p + 2 * i);
+        v[i] = t.x;
+        v[i + 1] = t.y;
+    }
+}
+template <int P>
+__device__ __forceinline__ void write_states(float* p, const f32x2 (&v)[P])
+{
+#pragma unroll
+    for (int i = 0; i < P; i += 2) *reinterpret_cast<ulonglong2*>(p + 2 * i) = make_ulonglong2(v[i], v[i + 1]);
+}
+
 struct SsmDev {
     const void *x, *dt, *b, *c, *z;
     unsigned ldx, lddt, ldb, ldc, ldz;   // bytes from row to row
@@ -140,20 +181,6 @@ struct SsmDev {
     int D, G, tiles;   // tiles: channel tiles per group
     bool softplus, o_bf16;
 };
-
-// One tile of rows [t0, t0 + TT) of a token-major array into shared memory, 16
-// bytes at a time; rows from `stop` on and channels from `nvalid` on are zero.
-template <typename T, int TT, int COLS, int THREADS>
-__device__ __forceinline__ void fetch_rows(T* dst, const T* src, long long ld, long long t0, long long stop, int nvalid)
-{
-    constexpr int VE = 16 / sizeof(T), VPR = COLS / VE;
-    static_assert(COLS % VE == 0, "row of whole 16-byte vectors");
-    for (int i = threadIdx.x; i < TT * VPR; i += THREADS) {
-        const int r = i / VPR, v = (i % VPR) * VE;
-        const bool ok = t0 + r < stop && v < nvalid;
-        cp_async16(dst + r * COLS + v, ok ? src + (t0 + r) * ld + v : src, ok);
-    }
-}
 
 }  // namespace mixer
 }  // namespace kda

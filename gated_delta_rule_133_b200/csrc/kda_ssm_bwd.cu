@@ -9,6 +9,7 @@
 // a time into registers and runs the reverse recurrence over them; and two sums
 // in a fixed order, of dB and dC over channel tiles and of dA, dskip and dbias
 // over the blocks that share a channel.
+#include "kda_sm100.cuh"
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -22,232 +23,301 @@ struct BwdDev {
     float *part;              // [tile of the group][token][G][2 N]: dB, dC
     float *partA, *partv;     // [slot][D][N]; [slot][2][D]: dskip, dbias
     int slots;
+    long long timeout_cycles;
 };
 
-template <typename T, int N_, int L_, int CK_>
+// Shape of the reverse walk.  A channel's N states lie on L lanes, NPT each, so a
+// warp holds a set of DT channels; it takes TK tokens at a time and does so for
+// the SETS sets of a tile of 32 channels one after the other, with the sums of dB
+// and dC over the channels in registers.  W warps take turns along the sequence.
+template <int N_>
 struct Rev {
-    static constexpr int N = N_, L = L_, CK = CK_, NPT = N / L, DT = L == 4 ? 32 : 16, THREADS = DT * L;
-    static constexpr int TT = N == 64 ? 32 : L == 4 ? 32 : 64, WARPS = THREADS / 32, CPW = 32 / L, GT = L / 2;
-    static constexpr int EP = TT * DT / THREADS;
-    static constexpr int DUROW = 2 * DT + 16, DYROW = DT + 4;
-    static constexpr size_t RAW_X = (size_t)TT * DT * sizeof(T), RAW_B = (size_t)TT * N * sizeof(T);
-    static constexpr size_t RAW_G = (size_t)TT * DT * 4;
-    static constexpr size_t STAGE = 3 * RAW_X + 2 * RAW_B + RAW_G;
-    static constexpr size_t WORK = ((size_t)TT * (DUROW + DYROW + 2 * N) + (size_t)WARPS * CK * 2 * N) * 4;
-    static constexpr size_t SMEM = 2 * STAGE + WORK;
-    static_assert(CK % GT == 0 && TT % CK == 0, "groups");
+    static constexpr int N = N_, L = N == 16 ? 4 : 8, NPT = N / L, DT = 32 / L, TK = 32 / NPT, TILE = 32;
+    static constexpr int SETS = TILE / DT, W = N == 64 ? 8 : 12, THREADS = 32 * W;
+    static constexpr int V = 2 * NPT, VL = V / DT;          // values of dB, dC per token: of a lane, left to a lane
+    static constexpr int EL = TK * DT / 2;                  // lanes with a pair of channels outside the walk
+    static constexpr int DUROW = DT + 2, DYROW = DT + 2, BQ = TK * N / 128;
+    // floats of shared memory: per warp, and in all
+    template <typename T>
+    static constexpr int warp_floats()
+    {
+        return TK * (2 * DUROW + DYROW + 2 * DT) + 2 * TK * N * (int)sizeof(T) / 4;
+    }
+    template <typename T>
+    static constexpr size_t smem()
+    {
+        return 4 * ((size_t)W * warp_floats<T>() + SETS * 32 * NPT + 2 * (size_t)W * SETS * 32 * NPT +
+                    (size_t)W * SETS * EL * 4) + 8 * W * SETS + 16;
+    }
 };
 
-template <typename T, int N, int L, int CK>
-__global__ void __launch_bounds__(Rev<T, N, L, CK>::THREADS)
+// As in the forward walk, the warps of a block take turns, backwards in time: a
+// warp recomputes the states of its TK tokens from the checkpoint before them,
+// waits for the state gradient of the warp behind it (an mbarrier per warp and
+// set), runs the chain g = C dy0 + a g', hands it on, and then forms everything
+// else.  Sums over a channel's lanes (dx, dDelta) and over a warp's channels (dB,
+// dC) are transposed reductions, many values at a time.
+template <typename T, int N>
+__global__ void __launch_bounds__(Rev<N>::THREADS, 1)
 ssm_reverse_kernel(const BwdDev b)
 {
-    using K = Rev<T, N, L, CK>;
-    constexpr int TT = K::TT, DT = K::DT, NPT = K::NPT, EP = K::EP, NT = K::THREADS, GT = K::GT;
+    using K = Rev<N>;
+    constexpr int TK = K::TK, DT = K::DT, L = K::L, NPT = K::NPT, SETS = K::SETS, W = K::W, VL = K::VL, BQ = K::BQ;
     const SsmDev& p = b.p;
     extern __shared__ __align__(16) unsigned char smem[];
-    float* sDU = reinterpret_cast<float*>(smem + 2 * K::STAGE);
-    float* sDY = sDU + TT * K::DUROW;
-    float* sB = sDY + TT * K::DYROW;
-    float* sC = sB + TT * N;
-    float* sP = sC + TT * N;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = lane / L, l = lane % L;
+    float* base = reinterpret_cast<float*>(smem);
+    float* sA = base + W * K::template warp_floats<T>();                 // [set][lane][NPT]
+    float* sCarry = sA + SETS * 32 * NPT;                                // [warp][set][lane][NPT]
+    float* sGA = sCarry + W * SETS * 32 * NPT;                           // the same: sums of dA
+    float* sGP = sGA + W * SETS * 32 * NPT;                              // [warp][set][EL][4]: dskip, dbias of a pair
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sGP + W * SETS * K::EL * 4);   // [warp][set]
+    int* aborted = reinterpret_cast<int*>(bars + W * SETS);
+    float* mine = base + w * K::template warp_floats<T>();
+    float2* sDU = reinterpret_cast<float2*>(mine);                       // [token][channel]: Delta, u
+    float* sDY = mine + 2 * TK * K::DUROW;                               // [token][channel]: dy0
+    float* sS = sDY + TK * K::DYROW;                                     // [token][channel][2]: sums of g B, w A
+    T* sB = reinterpret_cast<T*>(sS + 2 * TK * DT);                      // [token][N]
+    T* sC = sB + TK * N;
 
     flag_bad_sequences(p.q);
     const int ntiles = p.tiles * p.G;
     const int tile = blockIdx.x % ntiles, slot = blockIdx.x / ntiles;
-    const int Dg = p.D / p.G, g = tile / p.tiles, gt = tile % p.tiles, off = gt * DT;
-    const int c0 = g * Dg + off, nvalid = min(DT, Dg - off);
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, l = tid % L, c = tid / L;
-    const bool live = c < nvalid;
+    const int Dg = p.D / p.G, g = tile / p.tiles, gt = tile % p.tiles, off = gt * K::TILE, c00 = g * Dg + off;
+    const int sets = min(SETS, (Dg - off) / DT);   // D / G is a multiple of 8: whole sets
 
-    const T* x = static_cast<const T*>(p.x) + c0;
-    const T* dt = static_cast<const T*>(p.dt) + c0;
-    const T* z = p.z ? static_cast<const T*>(p.z) + c0 : nullptr;
-    const T* bb = static_cast<const T*>(p.b) + g * N;
-    const T* cc = static_cast<const T*>(p.c) + g * N;
+    for (int i = threadIdx.x; i < SETS * 32 * NPT; i += K::THREADS) {
+        const int ch = i / N;   // [set][channel][N] is the same order as [set][lane][NPT]
+        sA[i] = ch < sets * DT ? p.A[(long long)(c00 + ch) * N + i % N] : 0.f;
+    }
+    for (int i = threadIdx.x; i < W * SETS * 32 * NPT; i += K::THREADS) sGA[i] = 0.f;
+    for (int i = threadIdx.x; i < W * SETS * K::EL * 4; i += K::THREADS) sGP[i] = 0.f;
+    if (threadIdx.x < W * SETS) sm100::mbar_init(bars + threadIdx.x, 1);
+    if (threadIdx.x == 0) {
+        *aborted = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
 
-    float A[NPT], gA[NPT];
-#pragma unroll
-    for (int n = 0; n < NPT; ++n) {
-        A[n] = live ? p.A[(long long)(c0 + c) * N + l * NPT + n] : 0.f;
-        gA[n] = 0.f;
-    }
-    const int rt = tid * EP / DT, rc = tid * EP % DT;
-    const bool rlive = rc < nvalid;
-    float bias[EP], skip[EP], gskip[EP], gbias[EP];
-#pragma unroll
-    for (int k = 0; k < EP; ++k) {
-        bias[k] = rlive && p.dt_bias ? p.dt_bias[c0 + rc + k] : 0.f;
-        skip[k] = rlive && p.skip ? p.skip[c0 + rc + k] : 0.f;
-        gskip[k] = gbias[k] = 0.f;
-    }
+    const bool gated = p.z != nullptr, el = lane < K::EL;
+    const int et = lane / (DT / 2), ec = lane % (DT / 2) * 2;   // the lane's pair outside the walk: token, channel of the set
+    const int from = (w + W - 1) % W;
+    unsigned parity = 0;
+    bool ok = true;   // no wait has run out
+    typedef typename Raw<T>::pair Pair;
+    typedef typename Raw<T>::quad Quad;
 
     for (int seq = slot; seq < p.q.n; seq += b.slots) {
         const long long s = p.q.begin(seq);
         long long e = p.q.begin(seq + 1);
         if (e < s || !Seqs::inside(s, e, p.q.tokens)) e = s;
-        auto fetch = [&](long long t0, int stage) {
-            T* st = reinterpret_cast<T*>(smem + stage * K::STAGE);
-            fetch_rows<T, TT, DT, NT>(st, x, p.ldx / sizeof(T), t0, e, nvalid);
-            fetch_rows<T, TT, DT, NT>(st + TT * DT, dt, p.lddt / sizeof(T), t0, e, nvalid);
-            if (z) fetch_rows<T, TT, DT, NT>(st + 2 * TT * DT, z, p.ldz / sizeof(T), t0, e, nvalid);
-            fetch_rows<T, TT, N, NT>(st + 3 * TT * DT, bb, p.ldb / sizeof(T), t0, e, N);
-            fetch_rows<T, TT, N, NT>(st + 3 * TT * DT + TT * N, cc, p.ldc / sizeof(T), t0, e, N);
-            fetch_rows<float, TT, DT, NT>(reinterpret_cast<float*>(st + 3 * TT * DT + 2 * TT * N), b.gy + c0, p.D, t0, e,
-                                          nvalid);
+        const int len = (int)(e - s), nb = (len + TK - 1) / TK, first = (int)s;
+        const long long ckpt0 = ckpt_base<TK>(p.q, seq, s);
+        const long long srow = ((long long)seq * p.D + c00) * N + lane * NPT;   // + set * 32 * NPT
+        if (nb == 0 && b.gs0 && w == 0) {
+            for (int o = 0; o < sets; ++o)
+#pragma unroll
+                for (int n = 0; n < NPT; ++n)
+                    b.gs0[srow + o * 32 * NPT + n] = b.gsT ? b.gsT[srow + o * 32 * NPT + n] : 0.f;
+        }
+
+        Pair nx, ndt, nz;
+        float2 ngy;
+        f32x2 nh[NPT / 2];
+        auto fetch = [&](int blk, int o) {   // set o of block blk (blk < 0: none left)
+            nx = ndt = nz = Pair{};
+            ngy = make_float2(0.f, 0.f);
+            if (blk < 0) return;
+            const int ch = c00 + o * DT + ec;
+            if (el && blk * TK + et < len) {
+                const unsigned t = first + blk * TK + et;
+                nx = *reinterpret_cast<const Pair*>(row<T>(p.x, t, p.ldx) + ch);
+                ndt = *reinterpret_cast<const Pair*>(row<T>(p.dt, t, p.lddt) + ch);
+                if (gated) nz = *reinterpret_cast<const Pair*>(row<T>(p.z, t, p.ldz) + ch);
+                ngy = *reinterpret_cast<const float2*>(row<float>(b.gy, t, 4u * p.D) + ch);
+            }
+            const float* cp = b.ckpt + ((ckpt0 + blk) * p.D + c00 + o * DT) * N + lane * NPT;
+            read_states(cp, nh);
         };
-        const long long srow = ((long long)seq * p.D + c0 + c) * N + l * NPT;
-        float carry[NPT];
-#pragma unroll
-        for (int n = 0; n < NPT; ++n) carry[n] = live && b.gsT ? b.gsT[srow + n] : 0.f;
+        if (w < nb) fetch(nb - 1 - w, 0);
 
-        int stage = 0;
-        long long t0 = s + (e - s - 1) / TT * TT;
-        if (s < e) fetch(t0, 0);
-        cp_async_commit();
-        for (; s < e && t0 >= s; t0 -= TT, stage ^= 1) {
-            if (t0 > s) fetch(t0 - TT, stage ^ 1);
-            cp_async_commit();
-            cp_async_wait<1>();
-            __syncthreads();
-            const T* st = reinterpret_cast<const T*>(smem + stage * K::STAGE);
-            const float* sg = reinterpret_cast<const float*>(st + 3 * TT * DT + 2 * TT * N);
-            const bool rin = rlive && t0 + rt < e;
-            float xv[EP], delta[EP], dy[EP];
-            load_vec<EP>(st + rt * DT + rc, xv);
-            {
-                float v[EP];
-                load_vec<EP>(st + TT * DT + rt * DT + rc, v);
+        for (int r = w; ok && r < nb; r += W) {
+            const int blk = nb - 1 - r, t0 = blk * TK;
+            __syncwarp();
 #pragma unroll
-                for (int k = 0; k < EP; ++k) {
-                    v[k] += bias[k];
-                    delta[k] = !rin ? 0.f : p.softplus ? softplus(v[k]) : v[k];
-                    *reinterpret_cast<float2*>(sDU + rt * K::DUROW + 2 * (rc + k)) =
-                        make_float2(delta[k], delta[k] * xv[k]);
+            for (int q = 0; q < BQ; ++q) {
+                const int i = q * 32 + lane, t = t0 + i / (N / 4), n = g * N + i % (N / 4) * 4;
+                Quad vb{}, vc{};
+                if (t < len) {
+                    vb = *reinterpret_cast<const Quad*>(row<T>(p.b, first + t, p.ldb) + n);
+                    vc = *reinterpret_cast<const Quad*>(row<T>(p.c, first + t, p.ldc) + n);
                 }
-                load_vec<EP>(sg + rt * DT + rc, dy);
-                if (z) {
-                    load_vec<EP>(st + 2 * TT * DT + rt * DT + rc, v);
-#pragma unroll
-                    for (int k = 0; k < EP; ++k) dy[k] *= silu(v[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < EP; ++k) {
-                    dy[k] = rin ? dy[k] : 0.f;
-                    sDY[rt * K::DYROW + rc + k] = dy[k];
-                }
+                reinterpret_cast<Quad*>(sB)[i] = vb;
+                reinterpret_cast<Quad*>(sC)[i] = vc;
             }
-            for (int i = tid * 2; i < TT * N; i += 2 * NT) {
-                float v[2];
-                load_vec<2>(st + 3 * TT * DT + i, v);
-                store_vec<2>(sB + i, v);
-                load_vec<2>(st + 3 * TT * DT + TT * N + i, v);
-                store_vec<2>(sC + i, v);
-            }
-            __syncthreads();
+            float acc[TK][VL];
+#pragma unroll
+            for (int j = 0; j < TK; ++j)
+#pragma unroll
+                for (int v = 0; v < VL; ++v) acc[j][v] = 0.f;
 
-            for (int tb = (int)(min((long long)TT, e - t0) - 1) / CK * CK; tb >= 0; tb -= CK) {
-                float h0[NPT], a[CK][NPT], h[CK][NPT];
-                const float* cp = b.ckpt + ((ckpt_base<CK>(p.q, seq, s) + (t0 - s + tb) / CK) * p.D + c0 + c) * N + l * NPT;
+            for (int o = 0; o < sets; ++o) {
+                // the pair's elements
+                const float2 x = widen(nx), z = widen(nz), raw = widen(ndt);
+                float2 dy = ngy, v = raw, bias = make_float2(0.f, 0.f), delta;
+                const int ch = c00 + o * DT + ec;
+                if (p.dt_bias && el) bias = *reinterpret_cast<const float2*>(p.dt_bias + ch);
+                v.x += bias.x;
+                v.y += bias.y;
+                delta = v;
+                if (p.softplus) unpack(softplus2(v.x, v.y), delta.x, delta.y);
+                if (t0 + et >= len) delta = make_float2(0.f, 0.f);   // (x and gy are zero there)
+                if (gated) {
+                    dy.x *= silu(z.x);
+                    dy.y *= silu(z.y);
+                }
+                f32x2 h0[NPT / 2];
 #pragma unroll
-                for (int n = 0; n < NPT; ++n) h0[n] = live ? cp[n] : 0.f;
+                for (int n = 0; n < NPT / 2; ++n) h0[n] = nh[n];
+                if (el) {
+                    *reinterpret_cast<float4*>(&sDU[et * K::DUROW + ec]) =
+                        make_float4(delta.x, delta.x * x.x, delta.y, delta.y * x.y);
+                    *reinterpret_cast<float2*>(&sDY[et * K::DYROW + ec]) = dy;
+                }
+                __syncwarp();
+                fetch(o + 1 < sets ? blk : blk - W, o + 1 < sets ? o + 1 : 0);
+
+                f32x2 A[NPT / 2], a[TK][NPT / 2], h[TK][NPT / 2], q[TK][NPT / 2];
+                read_states(sA + (o * 32 + lane) * NPT, A);
 #pragma unroll
-                for (int j = 0; j < CK; ++j) {
-                    const float2 du = *reinterpret_cast<const float2*>(sDU + (tb + j) * K::DUROW + 2 * c);
+                for (int j = 0; j < TK; ++j) {
+                    const float2 du = sDU[j * K::DUROW + c];
+                    const float d = sDY[j * K::DYROW + c];
+                    f32x2 B[NPT / 2], C[NPT / 2];
+                    read_states(sB + j * N + l * NPT, B);
+                    read_states(sC + j * N + l * NPT, C);
 #pragma unroll
-                    for (int n = 0; n < NPT; ++n) {
-                        a[j][n] = exp2_approx(fmaf(du.x, A[n] * kLog2e, kDecayShift));
-                        h[j][n] = fmaf(a[j][n], j ? h[j - 1][n] : h0[n], du.y * sB[(tb + j) * N + l * NPT + n]);
+                    for (int n = 0; n < NPT / 2; ++n) {
+                        a[j][n] = decay2(pack(du.x, du.x), mul2(A[n], pack(kLog2e, kLog2e)));
+                        h[j][n] = fma2(a[j][n], j ? h[j > 0 ? j - 1 : 0][n] : h0[n], mul2(pack(du.y, du.y), B[n]));
+                        q[j][n] = mul2(C[n], pack(d, d));
                     }
                 }
+                f32x2 cr[NPT / 2];
+                if (r > 0) {
+                    ok = sm100::mbar_wait(bars + from * SETS + o, parity, aborted, b.timeout_cycles);
+                    if (!ok) break;
+                    read_states(sCarry + ((from * SETS + o) * 32 + lane) * NPT, cr);
+                } else {
 #pragma unroll
-                for (int jg = CK - GT; jg >= 0; jg -= GT) {
-                    float sums[2 * GT];
+                    for (int n = 0; n < NPT / 2; ++n)
+                        cr[n] = b.gsT ? *reinterpret_cast<const f32x2*>(b.gsT + srow + o * 32 * NPT + 2 * n) : 0ull;
+                }
+                // q becomes g, and a the gradient handed to the token before: a g
 #pragma unroll
-                    for (int jj = GT - 1; jj >= 0; --jj) {
-                        const int j = jg + jj, t = tb + j;
-                        const float2 du = *reinterpret_cast<const float2*>(sDU + t * K::DUROW + 2 * c);
-                        const float d = sDY[t * K::DYROW + c];
-                        float v[2 * NPT], s1 = 0.f, s2 = 0.f;
+                for (int j = TK - 1; j >= 0; --j)
 #pragma unroll
-                        for (int n = 0; n < NPT; ++n) {
-                            const float gh = fmaf(sC[t * N + l * NPT + n], d, carry[n]);
-                            v[n] = gh * du.y;
-                            v[NPT + n] = h[j][n] * d;
-                            s1 = fmaf(gh, sB[t * N + l * NPT + n], s1);
-                            carry[n] = gh * a[j][n];
-                            const float w = carry[n] * (j ? h[j > 0 ? j - 1 : 0][n] : h0[n]);
-                            gA[n] = fmaf(w, du.x, gA[n]);
-                            s2 = fmaf(w, A[n], s2);
-                        }
-                        sums[2 * jj] = s1;
-                        sums[2 * jj + 1] = s2;
-                        // over the warp's channels: dB, dC of this token
-                        reduce_transposed<2 * NPT, K::CPW, L>(v, lane);
-                        constexpr int VPL = 2 * NPT / K::CPW;   // values this lane is left with
-                        const int i0 = (lane / L) * VPL;
-                        float* o = sP + (wid * CK + j) * 2 * N + (i0 / NPT) * N + l * NPT + i0 % NPT;
-#pragma unroll
-                        for (int k = 0; k < VPL; ++k) o[k] = v[k];
+                    for (int n = 0; n < NPT / 2; ++n) {
+                        q[j][n] = add2(q[j][n], cr[n]);
+                        cr[n] = a[j][n] = mul2(a[j][n], q[j][n]);
                     }
-                    reduce_transposed<2 * GT, L, 1>(sums, lane);
+                if (blk > 0) {
+                    write_states(sCarry + ((w * SETS + o) * 32 + lane) * NPT, cr);
                     __syncwarp();
-                    // every lane of the channel has read (Delta, u) of these GT tokens
-                    sDU[(tb + jg + l / 2) * K::DUROW + 2 * c + (l & 1)] = sums[0];
-                }
-                __syncthreads();
-                for (int i = tid; i < CK * 2 * N; i += NT) {
-                    const long long t = t0 + tb + i / (2 * N);
-                    if (t < e) {
-                        float acc = sP[i];
+                    if (lane == 0) sm100::mbar_arrive(bars + w * SETS + o);
+                } else if (b.gs0) {
 #pragma unroll
-                        for (int w = 1; w < K::WARPS; ++w) acc += sP[w * CK * 2 * N + i];
-                        b.part[(((long long)gt * p.q.tokens + t) * p.G + g) * 2 * N + i % (2 * N)] = acc;
+                    for (int n = 0; n < NPT / 2; ++n) *reinterpret_cast<f32x2*>(b.gs0 + srow + o * 32 * NPT + 2 * n) = cr[n];
+                }
+
+                f32x2 gA[NPT / 2];
+                read_states(sGA + ((w * SETS + o) * 32 + lane) * NPT, gA);
+                constexpr int GT = L / 2;   // tokens whose two sums fill the channel's lanes
+#pragma unroll
+                for (int jg = 0; jg < TK; jg += GT) {
+                    float sums[L];
+#pragma unroll
+                    for (int jj = 0; jj < GT; ++jj) {
+                        const int j = jg + jj;
+                        const float2 du = sDU[j * K::DUROW + c];
+                        const float d = sDY[j * K::DYROW + c];
+                        f32x2 B[NPT / 2], s1 = 0ull, s2 = 0ull;
+                        read_states(sB + j * N + l * NPT, B);
+                        float val[K::V];
+#pragma unroll
+                        for (int n = 0; n < NPT / 2; ++n) {
+                            unpack(mul2(q[j][n], pack(du.y, du.y)), val[2 * n], val[2 * n + 1]);
+                            unpack(mul2(h[j][n], pack(d, d)), val[NPT + 2 * n], val[NPT + 2 * n + 1]);
+                            s1 = n ? fma2(q[j][n], B[n], s1) : mul2(q[j][n], B[n]);
+                            const f32x2 wt = mul2(a[j][n], j ? h[j > 0 ? j - 1 : 0][n] : h0[n]);
+                            gA[n] = fma2(wt, pack(du.x, du.x), gA[n]);
+                            s2 = n ? fma2(wt, A[n], s2) : mul2(wt, A[n]);
+                        }
+                        reduce_transposed<K::V, DT, L>(val, lane);
+#pragma unroll
+                        for (int k = 0; k < VL; ++k) acc[j][k] += val[k];
+                        float lo, hi;
+                        unpack(s1, lo, hi);
+                        sums[2 * jj] = lo + hi;
+                        unpack(s2, lo, hi);
+                        sums[2 * jj + 1] = lo + hi;
                     }
+                    reduce_transposed<L, L, 1>(sums, lane);
+                    sS[((jg + l / 2) * DT + c) * 2 + (l & 1)] = sums[0];
                 }
-                __syncthreads();
-            }
-            if (rin) {
-                const long long o = (t0 + rt) * p.D + c0 + rc;
-                float gx[EP], gd[EP], v[EP];
-                load_vec<EP>(st + TT * DT + rt * DT + rc, v);
-#pragma unroll
-                for (int k = 0; k < EP; ++k) {
-                    const float2 ss = *reinterpret_cast<const float2*>(sDU + rt * K::DUROW + 2 * (rc + k));
-                    gx[k] = fmaf(ss.x, delta[k], skip[k] * dy[k]);
-                    gd[k] = fmaf(ss.x, xv[k], ss.y) * (p.softplus ? sigmoid(v[k] + bias[k]) : 1.f);
-                    gskip[k] = fmaf(dy[k], xv[k], gskip[k]);
-                    gbias[k] += gd[k];
+                write_states(sGA + ((w * SETS + o) * 32 + lane) * NPT, gA);
+                __syncwarp();
+                if (el && t0 + et < len) {
+                    const float4 ss = *reinterpret_cast<const float4*>(sS + (et * DT + ec) * 2);   // s1, s2 of both channels
+                    float2 skip = make_float2(0.f, 0.f);
+                    if (p.skip) skip = *reinterpret_cast<const float2*>(p.skip + ch);
+                    const unsigned t = first + t0 + et;
+                    float2 gx, gd;
+                    gx.x = fmaf(ss.x, delta.x, skip.x * dy.x);
+                    gx.y = fmaf(ss.z, delta.y, skip.y * dy.y);
+                    gd.x = fmaf(ss.x, x.x, ss.y) * (p.softplus ? sigmoid(v.x) : 1.f);
+                    gd.y = fmaf(ss.z, x.y, ss.w) * (p.softplus ? sigmoid(v.y) : 1.f);
+                    *reinterpret_cast<float2*>(row<float>(b.gx, t, 4u * p.D) + ch) = gx;
+                    *reinterpret_cast<float2*>(row<float>(b.gdt, t, 4u * p.D) + ch) = gd;
+                    float4* gp = reinterpret_cast<float4*>(sGP + ((w * SETS + o) * K::EL + lane) * 4);
+                    float4 f = *gp;
+                    f.x = fmaf(dy.x, x.x, f.x);
+                    f.y = fmaf(dy.y, x.y, f.y);
+                    f.z += gd.x;
+                    f.w += gd.y;
+                    *gp = f;
                 }
-                store_vec<EP>(b.gx + o, gx);
-                store_vec<EP>(b.gdt + o, gd);
+                __syncwarp();   // the warp's arrays are free
             }
-            __syncthreads();   // the stage and the work arrays are free
-        }
-        if (b.gs0 && live) {
+            if (!ok) break;
+            if (r > 0) parity ^= 1u;
+            // dB, dC of the tile's channels: values i0 .. of (dB, dC) x NPT states
+            const int i0 = lane / L * VL, col = i0 / NPT * N + l * NPT + i0 % NPT;
 #pragma unroll
-            for (int n = 0; n < NPT; ++n) b.gs0[srow + n] = carry[n];
+            for (int j = 0; j < TK; ++j) {
+                if (t0 + j < len) {
+                    float* o = b.part + (((long long)gt * p.q.tokens + first + t0 + j) * p.G + g) * 2 * N + col;
+#pragma unroll
+                    for (int k = 0; k < VL; ++k) o[k] = acc[j][k];
+                }
+            }
         }
+        __syncthreads();   // the next sequence starts with every hand-over taken
     }
 
-    // this block's sums over its tokens
-    if (live) {
-#pragma unroll
-        for (int n = 0; n < NPT; ++n) b.partA[((long long)slot * p.D + c0 + c) * N + l * NPT + n] = gA[n];
+    // this block's sums over its tokens: the warps' sums in order
+    for (int i = threadIdx.x; i < sets * 32 * NPT; i += K::THREADS) {
+        float sum = 0.f;
+        for (int v = 0; v < W; ++v) sum += sGA[v * SETS * 32 * NPT + i];
+        b.partA[((long long)slot * p.D + c00) * N + i] = sum;
     }
-    __syncthreads();
-    float* red = sDU;   // [TT][2 DT]: TT rows of threads share a channel vector
-    static_assert(K::DUROW >= 2 * DT, "room");
-#pragma unroll
-    for (int k = 0; k < EP; ++k) {
-        red[rt * 2 * DT + rc + k] = gskip[k];
-        red[rt * 2 * DT + DT + rc + k] = gbias[k];
-    }
-    __syncthreads();
-    for (int i = tid; i < 2 * DT; i += NT) {
-        float acc = 0.f;
-        for (int r = 0; r < TT; ++r) acc += red[r * 2 * DT + i];
-        if (i % DT < nvalid) b.partv[((long long)slot * 2 + i / DT) * p.D + c0 + i % DT] = acc;
+    for (int i = threadIdx.x; i < sets * DT * 2; i += K::THREADS) {
+        const int ch = i / 2, which = i % 2, o = ch / DT, cc = ch % DT;
+        float sum = 0.f;
+        for (int v = 0; v < W; ++v)
+            for (int t = 0; t < TK; ++t)
+                sum += sGP[((v * SETS + o) * K::EL + t * (DT / 2) + cc / 2) * 4 + which * 2 + cc % 2];
+        b.partv[((long long)slot * 2 + which) * p.D + c00 + ch] = sum;
     }
 }
 
@@ -301,18 +371,16 @@ ssm_bwd_params_kernel(const BwdDev b, float* __restrict__ gA, float* __restrict_
     }
 }
 
+// Budget of a wait for the next warp's state, in SM clock cycles (about a second).
+constexpr long long kBwdTimeoutCycles = 1LL << 31;
+
 // Sequences are dealt to this many blocks per channel tile: enough to fill the
 // 148 SMs several times, few enough that the partial sums of dA stay small.
 static int bwd_slots(int nseq, int ntiles)
 {
-    const int want = (148 * 8 + ntiles - 1) / ntiles;
+    const int want = (148 * 4 + ntiles - 1) / ntiles;
     return nseq < want ? nseq : want;
 }
-
-template <int N>
-struct BwdShape {
-    static constexpr int L = N == 64 ? 16 : 8, CK = 8, DT = 16;
-};
 
 struct BwdWorkspace {
     size_t ckpt, part, partA, partv, total;
@@ -321,9 +389,9 @@ struct BwdWorkspace {
 template <int N>
 static BwdWorkspace bwd_layout(int nseq, int T, long long tokens, int D, int G, bool varlen)
 {
-    using S = BwdShape<N>;
-    const int tiles = (D / G + S::DT - 1) / S::DT, slots = bwd_slots(nseq, tiles * G);
-    const size_t blocks = varlen ? (size_t)(tokens / S::CK) + nseq : (size_t)nseq * ((T + S::CK - 1) / S::CK);
+    using K = Rev<N>;
+    const int tiles = (D / G + K::TILE - 1) / K::TILE, slots = bwd_slots(nseq, tiles * G);
+    const size_t blocks = varlen ? (size_t)(tokens / K::TK) + nseq : (size_t)nseq * ((T + K::TK - 1) / K::TK);
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     BwdWorkspace w;
     w.ckpt = 0;
@@ -337,9 +405,7 @@ static BwdWorkspace bwd_layout(int nseq, int T, long long tokens, int D, int G, 
 template <typename T, int N>
 static cudaError_t launch_bwd(const SsmArgs& a, const SsmGrads& g, void* ws, cudaStream_t s)
 {
-    using S = BwdShape<N>;
-    using K = Rev<T, N, S::L, S::CK>;
-    static_assert(K::DT == S::DT, "channel tile");
+    using K = Rev<N>;
     const BwdWorkspace w = bwd_layout<N>(a.nseq, a.T, a.tokens, a.D, a.G, a.cu != nullptr);
     char* base = static_cast<char*>(ws);
     BwdDev b;
@@ -350,15 +416,16 @@ static cudaError_t launch_bwd(const SsmArgs& a, const SsmGrads& g, void* ws, cud
     b.part = reinterpret_cast<float*>(base + w.part);
     b.partA = reinterpret_cast<float*>(base + w.partA);
     b.partv = reinterpret_cast<float*>(base + w.partv);
-    b.p.tiles = (a.D / a.G + S::DT - 1) / S::DT;
+    b.p.tiles = (a.D / a.G + K::TILE - 1) / K::TILE;
     b.slots = bwd_slots(a.nseq, b.p.tiles * a.G);
-    cudaError_t e = launch_walk<T, N, S::CK>(a, b.p, s,
+    b.timeout_cycles = kBwdTimeoutCycles;
+    cudaError_t e = launch_walk<T, N, K::TK>(a, b.p, s,
                                                     WalkBwd{g.gy, g.gz, reinterpret_cast<float*>(base + w.ckpt)});
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(ssm_reverse_kernel<T, N, S::L, S::CK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)K::SMEM);
+    e = cudaFuncSetAttribute(ssm_reverse_kernel<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)K::template smem<T>());
     if (e != cudaSuccess) return e;
-    ssm_reverse_kernel<T, N, S::L, S::CK><<<(unsigned)(b.slots * b.p.tiles * a.G), K::THREADS, K::SMEM, s>>>(b);
+    ssm_reverse_kernel<T, N><<<(unsigned)(b.slots * b.p.tiles * a.G), K::THREADS, K::template smem<T>(), s>>>(b);
     ssm_bwd_bc_kernel<<<(unsigned)((a.tokens + 7) / 8), 256, 0, s>>>(b, g.gb, g.gc, N);
     ssm_bwd_params_kernel<<<(unsigned)(((long long)a.D * (N + 2) + 255) / 256), 256, 0, s>>>(b, g.gA, g.gskip,
                                                                                              g.gdt_bias, N);
