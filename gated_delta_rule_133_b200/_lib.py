@@ -56,10 +56,8 @@ SIGNATURES = {
     "kda_conv_bwd": (_I, [_P, _L] + [_P] * 9 + [_I] * 6 + [_P, _Z, _P]),
     "kda_conv_varlen_bwd": (_I, [_P, _L] + [_P] * 3 + [_I] + [_P] * 7 + [_I] * 5 + [_P, _Z, _P]),
     "kda_conv_bwd_workspace_size": (_I, [_L, _I, _I, _ZP]),
-    "kda_ssm_fwd": (_I, _SSM_IN + [_P] * 3 + [_I] * 8 + [_P, _Z, _P]),
-    "kda_ssm_fwd_workspace_size": (_I, [_I] * 6 + [_ZP]),
-    "kda_ssm_varlen_fwd": (_I, _SSM_IN + [_P, _I] + [_P] * 3 + [_I] * 7 + [_P, _Z, _P]),
-    "kda_ssm_varlen_fwd_workspace_size": (_I, [_I] * 6 + [_ZP]),
+    "kda_ssm_fwd": (_I, _SSM_IN + [_P] * 3 + [_I] * 8 + [_P]),
+    "kda_ssm_varlen_fwd": (_I, _SSM_IN + [_P, _I] + [_P] * 3 + [_I] * 7 + [_P]),
     "kda_ssm_step": (_I, _SSM_IN + [_P] * 2 + [_I] * 7 + [_P]),
     "kda_ssm_bwd": (_I, _SSM_IN + [_P] * 12 + [_I] * 7 + [_P, _Z, _P]),
     "kda_ssm_bwd_workspace_size": (_I, [_I] * 6 + [_ZP]),

@@ -6,28 +6,17 @@
 //
 // Every path is bound by HBM: each input element is read once and each output
 // element written once (plus a halo of W - 1 rows per token tile, which the L2
-// holds).  A thread owns a 16-byte vector of channels and walks a tile of
-// tokens with the last W - 1 rows and the weights in registers, so no shared
-// memory or synchronisation is needed and the loads of the next tokens are in
-// flight together.
+// holds).  A thread owns four channels and walks a tile of tokens with the last
+// W - 1 rows and the weights in registers, so no shared memory or synchronisation
+// is needed and the loads of the next tokens are in flight together.  (Eight
+// channels per thread halve the requests but need twice the registers: 198, and
+// half the warps.)
 #include "kda_mixer.cuh"
 
 namespace kda {
 namespace mixer {
 
-// 16 bytes of T as fp32.
-template <typename T, int V>
-__device__ __forceinline__ void raw_to_float(const uint4& r, float (&x)[V])
-{
-    if constexpr (sizeof(T) == 2) {
-        static_assert(V == 8, "vector width");
-        unpack2(r.x, x[0], x[1]); unpack2(r.y, x[2], x[3]); unpack2(r.z, x[4], x[5]); unpack2(r.w, x[6], x[7]);
-    } else {
-        static_assert(V == 4, "vector width");
-        x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
-        x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
-    }
-}
+constexpr int kV = 4;   // channels per thread
 
 template <int W, int V>
 __device__ __forceinline__ void load_taps(const float* __restrict__ w, const float* __restrict__ bias, int c,
@@ -67,42 +56,68 @@ template <typename T, int W>
 __device__ __forceinline__ void write_state(const T* __restrict__ x, long long ldx, const T* s0, T* sT,
                                             const Seqs& q, int i, int D, int c)
 {
+    typedef typename Raw<T>::quad Quad;
     long long s = q.begin(i), e = q.begin(i + 1);
     if (e < s || !Seqs::inside(s, e, q.tokens)) e = s;
-    uint4 rows[W - 1];
+    Quad rows[W - 1];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         const long long pos = e - s - (W - 1) + j;
+        rows[j] = Quad{};
         if (pos >= 0)
-            rows[j] = *reinterpret_cast<const uint4*>(x + (s + pos) * ldx + c);
+            rows[j] = *reinterpret_cast<const Quad*>(x + (s + pos) * ldx + c);
         else if (s0)
-            rows[j] = *reinterpret_cast<const uint4*>(s0 + ((long long)i * (W - 1) + pos + W - 1) * D + c);
-        else
-            rows[j] = make_uint4(0u, 0u, 0u, 0u);
+            rows[j] = *reinterpret_cast<const Quad*>(s0 + ((long long)i * (W - 1) + pos + W - 1) * D + c);
     }
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-        *reinterpret_cast<uint4*>(sT + ((long long)i * (W - 1) + j) * D + c) = rows[j];
+    for (int j = 0; j < W - 1; ++j) *reinterpret_cast<Quad*>(sT + ((long long)i * (W - 1) + j) * D + c) = rows[j];
 }
 
 template <typename T, int W>
 __global__ void __launch_bounds__(128)
 conv_state_kernel(const T* __restrict__ x, long long ldx, const T* s0, T* sT, Seqs q, int D)
 {
-    constexpr int V = 16 / sizeof(T);
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kV;
     if (c < D) write_state<T, W>(x, ldx, s0, sT, q, blockIdx.x, D, c);
+}
+
+// The taps as pairs of channels.
+template <int W>
+__device__ __forceinline__ void load_taps2(const float* __restrict__ w, const float* __restrict__ bias, int c,
+                                           f32x2 (&wt)[W][2], f32x2 (&bv)[2])
+{
+    float f[W][kV], g[kV];
+    load_taps<W, kV>(w, bias, c, f, g);
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) wt[j][v] = pack(f[j][2 * v], f[j][2 * v + 1]);
+        bv[v] = pack(g[2 * v], g[2 * v + 1]);
+    }
+}
+
+template <bool SILU, typename TO>
+__device__ __forceinline__ void put(TO* y, const f32x2 (&p)[2])
+{
+    float out[kV];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        unpack(p[v], out[2 * v], out[2 * v + 1]);
+        if (SILU) unpack(silu2(out[2 * v], out[2 * v + 1]), out[2 * v], out[2 * v + 1]);
+    }
+    store_vec<kV>(y, out);
 }
 
 // Grid: x = token tiles of R tokens, then (if sT) one block per sequence for
 // the final states; y = channel blocks.  U tokens are loaded ahead.
 template <typename T, typename TO, int W, bool SILU>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 6)
 conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ bias,
                 const T* s0, TO* __restrict__ y, T* sT, Seqs q, int D, int R, int ntiles)
 {
-    constexpr int V = 16 / sizeof(T), U = 8;
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    constexpr int U = 8;
+    typedef typename Raw<T>::quad Quad;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kV;
     if ((int)blockIdx.x >= ntiles) {
         if (c < D) write_state<T, W>(x, ldx, s0, sT, q, blockIdx.x - ntiles, D, c);
         return;
@@ -113,8 +128,8 @@ conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
     int i = max(find_sequence(q, t), 0);
     if (c >= D) return;
 
-    float wt[W][V], bv[V];
-    load_taps<W, V>(w, bias, c, wt, bv);
+    f32x2 wt[W][2], bv[2];
+    load_taps2<W>(w, bias, c, wt, bv);
     for (; i < q.n && t < t1; ++i) {
         const long long s = q.begin(i), e = q.begin(i + 1);
         if (e <= t || e <= s) continue;
@@ -125,73 +140,85 @@ conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
             t = max(t, stop);
             continue;
         }
-        float win[W - 1][V];
+        f32x2 win[W - 1][2];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) load_row<T, W, V>(x, ldx, s0, s, i, t - s - (W - 1) + j, D, c, win[j]);
-        for (; t < stop; t += U) {
-            uint4 raw[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u < stop) raw[u] = *reinterpret_cast<const uint4*>(x + (t + u) * ldx + c);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (t + u < stop) {
-                    float xv[V], out[V];
-                    raw_to_float<T, V>(raw[u], xv);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        float p = fmaf(wt[W - 1][v], xv[v], bv[v]);
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) p = fmaf(wt[j][v], win[j][v], p);
-                        out[v] = SILU ? silu(p) : p;
-#pragma unroll
-                        for (int j = 0; j + 1 < W - 1; ++j) win[j][v] = win[j + 1][v];
-                        win[W - 2][v] = xv[v];
-                    }
-                    store_vec<V>(y + (t + u) * D + c, out);
-                }
-            }
+        for (int j = 0; j < W - 1; ++j) {
+            float f[kV];
+            load_row<T, W, kV>(x, ldx, s0, s, i, t - s - (W - 1) + j, D, c, f);
+            win[j][0] = pack(f[0], f[1]);
+            win[j][1] = pack(f[2], f[3]);
         }
+        const T* px = x + t * ldx + c;
+        TO* py = y + t * D + c;
+        auto step = [&](const Quad& raw) {
+            f32x2 xv[2], p[2];
+            widen(raw, xv);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                p[v] = fma2(wt[W - 1][v], xv[v], bv[v]);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) p[v] = fma2(wt[j][v], win[j][v], p[v]);
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j) win[j][v] = win[j + 1][v];
+                win[W - 2][v] = xv[v];
+            }
+            put<SILU>(py, p);
+            py += D;
+        };
+        int n = (int)(stop - t);
+#pragma unroll 1
+        for (; n >= U; n -= U) {
+            Quad raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u, px += ldx) raw[u] = *reinterpret_cast<const Quad*>(px);
+#pragma unroll
+            for (int u = 0; u < U; ++u) step(raw[u]);
+        }
+#pragma unroll 1
+        for (; n > 0; --n, px += ldx) step(*reinterpret_cast<const Quad*>(px));
         t = stop;
     }
 }
 
 // One token per sequence: y from the state's rows and x; the state moves up by
-// one row.  A thread owns a channel vector of RN sequences, so that the
-// weights are read once for them.
-template <typename T, typename TO, int W, bool SILU>
+// one row.  A thread owns a channel vector of RN sequences, so that the weights
+// are read once for them and all their rows are in flight together.
+template <typename T, typename TO, int W, bool SILU, int RN>
 __global__ void __launch_bounds__(128)
 conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ bias,
-                 T* __restrict__ state, TO* __restrict__ y, int n, int D, int RN)
+                 T* __restrict__ state, TO* __restrict__ y, int n, int D)
 {
-    constexpr int V = 16 / sizeof(T);
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    typedef typename Raw<T>::quad Quad;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kV;
     if (c >= D) return;
-    float wt[W][V], bv[V];
-    load_taps<W, V>(w, bias, c, wt, bv);
-    const int i1 = min((int)(blockIdx.x + 1) * RN, n);
-    for (int i = blockIdx.x * RN; i < i1; ++i) {
-        T* st = state + (long long)i * (W - 1) * D + c;
-        uint4 raw[W];
+    const int i0 = blockIdx.x * RN;
+    Quad raw[RN][W];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) raw[j] = *reinterpret_cast<const uint4*>(st + (long long)j * D);
-        raw[W - 1] = *reinterpret_cast<const uint4*>(x + i * ldx + c);
-        float out[V];
+    for (int r = 0; r < RN; ++r) {
+        if (i0 + r < n) {
+            const T* st = state + (long long)(i0 + r) * (W - 1) * D + c;
 #pragma unroll
-        for (int v = 0; v < V; ++v) out[v] = bv[v];
-#pragma unroll
-        for (int j = W - 1; j >= 0; --j) {
-            float xv[V];
-            raw_to_float<T, V>(raw[j], xv);
-#pragma unroll
-            for (int v = 0; v < V; ++v) out[v] = fmaf(wt[j][v], xv[v], out[v]);
-            if (j > 0) *reinterpret_cast<uint4*>(st + (long long)(j - 1) * D) = raw[j];
+            for (int j = 0; j < W - 1; ++j) raw[r][j] = *reinterpret_cast<const Quad*>(st + (long long)j * D);
+            raw[r][W - 1] = *reinterpret_cast<const Quad*>(x + (i0 + r) * ldx + c);
         }
-        if (SILU) {
+    }
+    f32x2 wt[W][2], bv[2];
+    load_taps2<W>(w, bias, c, wt, bv);
 #pragma unroll
-            for (int v = 0; v < V; ++v) out[v] = silu(out[v]);
+    for (int r = 0; r < RN; ++r) {
+        if (i0 + r < n) {
+            T* st = state + (long long)(i0 + r) * (W - 1) * D + c;
+            f32x2 p[2] = {bv[0], bv[1]};
+#pragma unroll
+            for (int j = W - 1; j >= 0; --j) {
+                f32x2 xv[2];
+                widen(raw[r][j], xv);
+                p[0] = fma2(wt[j][0], xv[0], p[0]);
+                p[1] = fma2(wt[j][1], xv[1], p[1]);
+                if (j > 0) *reinterpret_cast<Quad*>(st + (long long)(j - 1) * D) = raw[r][j];
+            }
+            put<SILU>(y + (long long)(i0 + r) * D + c, p);
         }
-        store_vec<V>(y + (long long)i * D + c, out);
     }
 }
 
@@ -203,29 +230,26 @@ conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict
 // its own gx but does not add to gw and gb).  gw and gb of a tile go to a
 // partial sum of its own, part[tile][j][D] (j = W: the bias), which a second
 // kernel adds in a fixed order: no atomics, the same result every time.
-constexpr int kBwdV = 4;   // channels per thread: 16-byte vectors of the fp32 gradients
-
 template <typename T, int W, bool SILU>
 __global__ void __launch_bounds__(128)
 conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ bias,
                 const T* __restrict__ s0, const float* __restrict__ gy, const float* __restrict__ gsT,
                 float* __restrict__ gx, float* __restrict__ part, Seqs q, int D, int R)
 {
-    constexpr int V = kBwdV, U = 4;
+    constexpr int U = 4;
+    typedef typename Raw<T>::quad Quad;
     flag_bad_sequences(q);
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kV;
     long long t = (long long)blockIdx.x * R;
     const long long t1 = min(t + R, q.tokens);
     int i = max(find_sequence(q, t), 0);
     if (c >= D) return;
 
-    float wt[W][V], bv[V], gw[W + 1][V];
-    load_taps<W, V>(w, bias, c, wt, bv);
+    f32x2 wt[W][2], bv[2], gw[W + 1][2];
+    load_taps2<W>(w, bias, c, wt, bv);
 #pragma unroll
-    for (int j = 0; j <= W; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) gw[j][v] = 0.f;
-    const float zero[V] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j <= W; ++j) gw[j][0] = gw[j][1] = 0ull;
+    const float zero[kV] = {0.f, 0.f, 0.f, 0.f};
 
     for (; t < t1; ++i) {
         long long s = q.tokens, e = q.tokens;   // behind the last sequence: rows of no sequence
@@ -236,100 +260,152 @@ conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
             if (e <= t || e <= s) continue;
             use = Seqs::inside(s, e, q.tokens);
         }
-        for (; t < min(s, t1); ++t) store_vec<V>(gx + t * D + c, zero);
+        for (; t < min(s, t1); ++t) store_vec<kV>(gx + t * D + c, zero);
         if (t >= t1) break;
         if (i >= q.n) break;
         const long long a = t, b = min(e, t1);
         if (!use) {   // a skipped sequence: zero gradient
-            for (; t < b; ++t) store_vec<V>(gx + t * D + c, zero);
+            for (; t < b; ++t) store_vec<kV>(gx + t * D + c, zero);
             continue;
         }
-        float win[W - 1][V], dp[W - 1][V];
+        f32x2 win[W - 1][2], dp[W - 1][2];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            load_row<T, W, V>(x, ldx, s0, s, i, a - s - (W - 1) + j, D, c, win[j]);
-#pragma unroll
-            for (int v = 0; v < V; ++v) dp[j][v] = 0.f;
+            float f[kV];
+            load_row<T, W, kV>(x, ldx, s0, s, i, a - s - (W - 1) + j, D, c, f);
+            win[j][0] = pack(f[0], f[1]);
+            win[j][1] = pack(f[2], f[3]);
+            dp[j][0] = dp[j][1] = 0ull;
         }
-        const long long load_end = min(b + W - 1, e);
-        for (; t < b + W - 1; t += U) {
-            float xs[U][V], gs[U][V];
+        const T* px = x + a * ldx + c;
+        const float* pg = gy + a * D + c;
+        // dpre of the next token (x, gy as loaded); `own`: it counts in gw and gb
+        auto slope = [&](const Quad& raw, const float4& g, bool own, f32x2 (&d)[2]) {
+            f32x2 xv[2];
+            widen(raw, xv);
+            d[0] = pack(g.x, g.y);
+            d[1] = pack(g.z, g.w);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (t + u < load_end) {
-                    load_vec<V>(x + (t + u) * ldx + c, xs[u]);
-                    load_vec<V>(gy + (t + u) * D + c, gs[u]);
-                } else {
+            for (int v = 0; v < 2; ++v) {
+                if (SILU) {
+                    f32x2 pre = fma2(wt[W - 1][v], xv[v], bv[v]);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) xs[u][v] = gs[u][v] = 0.f;
+                    for (int j = 0; j < W - 1; ++j) pre = fma2(wt[j][v], win[j][v], pre);
+                    float p0, p1;
+                    unpack(pre, p0, p1);
+                    d[v] = mul2(d[v], silu_grad2(p0, p1));
                 }
+                if (own) {
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) gw[j][v] = fma2(d[v], win[j][v], gw[j][v]);
+                    gw[W - 1][v] = fma2(d[v], xv[v], gw[W - 1][v]);
+                    gw[W][v] = add2(gw[W][v], d[v]);
+                }
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j) win[j][v] = win[j + 1][v];
+                win[W - 2][v] = xv[v];
+            }
+        };
+        // gx of the token W - 1 before the one with slope d: dp[k] is the slope k
+        // tokens after it
+        auto input_grad = [&](const f32x2 (&d)[2], f32x2 (&o)[2]) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                o[v] = mul2(wt[0][v], d[v]);
+#pragma unroll
+                for (int j = 1; j < W; ++j) o[v] = fma2(wt[j][v], dp[W - 1 - j][v], o[v]);
+            }
+        };
+        auto shift = [&](const f32x2 (&d)[2]) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j) dp[j][v] = dp[j + 1][v];
+                dp[W - 2][v] = d[v];
+            }
+        };
+        float* po = gx + a * D + c;
+        auto emit = [&](const f32x2 (&o)[2]) {
+            *reinterpret_cast<ulonglong2*>(po) = make_ulonglong2(o[0], o[1]);
+            po += D;
+        };
+        int n = (int)(b - a);
+        f32x2 d[2], o[2];
+        // the first W - 1 own tokens: their predecessors are another tile's
+        for (int k = 0; k < W - 1 && n > 0; ++k, --n, px += ldx, pg += D) {
+            slope(*reinterpret_cast<const Quad*>(px), *reinterpret_cast<const float4*>(pg), true, d);
+            shift(d);
+        }
+#pragma unroll 1
+        for (; n >= U; n -= U) {
+            Quad raw[U];
+            float4 g[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u, px += ldx, pg += D) {
+                raw[u] = *reinterpret_cast<const Quad*>(px);
+                g[u] = *reinterpret_cast<const float4*>(pg);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const long long p = t + u - (W - 1);
-                const bool own = t + u < b, emit = p >= a && p < b;
-                float out[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float pre = fmaf(wt[W - 1][v], xs[u][v], bv[v]);
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) pre = fmaf(wt[j][v], win[j][v], pre);
-                    const float d = t + u >= load_end ? 0.f : SILU ? gs[u][v] * silu_grad(pre) : gs[u][v];
-                    if (own) {
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) gw[j][v] = fmaf(d, win[j][v], gw[j][v]);
-                        gw[W - 1][v] = fmaf(d, xs[u][v], gw[W - 1][v]);
-                        gw[W][v] += d;
-                    }
-                    // dp[0] = dpre[p], ..., dp[W - 2] = dpre[p + W - 2], d = dpre[p + W - 1]
-                    float o = wt[0][v] * d;
-#pragma unroll
-                    for (int j = 1; j < W; ++j) o = fmaf(wt[j][v], dp[W - 1 - j][v], o);
-                    out[v] = o;
-#pragma unroll
-                    for (int j = 0; j + 1 < W - 1; ++j) {
-                        win[j][v] = win[j + 1][v];
-                        dp[j][v] = dp[j + 1][v];
-                    }
-                    win[W - 2][v] = xs[u][v];
-                    dp[W - 2][v] = d;
-                }
-                if (emit) {
-                    if (gsT && e - p <= W - 1) {
-                        float g[V];
-                        load_vec<V>(gsT + ((long long)i * (W - 1) + (W - 1) - (e - p)) * D + c, g);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) out[v] += g[v];
-                    }
-                    store_vec<V>(gx + p * D + c, out);
-                }
+                slope(raw[u], g[u], true, d);
+                input_grad(d, o);
+                shift(d);
+                emit(o);
             }
+        }
+#pragma unroll 1
+        for (; n > 0; --n, px += ldx, pg += D) {
+            slope(*reinterpret_cast<const Quad*>(px), *reinterpret_cast<const float4*>(pg), true, d);
+            input_grad(d, o);
+            shift(d);
+            emit(o);
+        }
+        // the W - 1 tokens after the last own one: the next tile's, or none and the
+        // final state's gradient instead
+#pragma unroll 1
+        for (long long u = b; u < b + W - 1; ++u, px += ldx, pg += D) {
+            d[0] = d[1] = 0ull;
+            if (u < e) slope(*reinterpret_cast<const Quad*>(px), *reinterpret_cast<const float4*>(pg), false, d);
+            if (u - (W - 1) >= a) {
+                input_grad(d, o);
+                if (u >= e && gsT) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(
+                        gsT + ((long long)i * (W - 1) + (u - e)) * D + c);
+                    o[0] = add2(o[0], f.x);
+                    o[1] = add2(o[1], f.y);
+                }
+                emit(o);
+            }
+            shift(d);
         }
         t = b;
     }
     float* o = part + (long long)blockIdx.x * (W + 1) * D + c;
 #pragma unroll
-    for (int j = 0; j <= W; ++j) store_vec<V>(o + (long long)j * D, gw[j]);
+    for (int j = 0; j <= W; ++j)
+        *reinterpret_cast<ulonglong2*>(o + (long long)j * D) = make_ulonglong2(gw[j][0], gw[j][1]);
 }
 
-// gw[d, j] and gb[d] from the tiles' partial sums: 32 columns per block, 8 rows
+// gw[d, j] and gb[d] from the tiles' partial sums: 32 columns per block, 32 rows
 // of threads over the tiles, then a sum over those rows.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
 conv_bwd_reduce_kernel(const float* __restrict__ part, int ntiles, float* __restrict__ gw, float* __restrict__ gb,
                        int D, int W)
 {
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     const int col = blockIdx.x * 32 + threadIdx.x;   // j * D + d
     const int ncol = (W + 1) * D;
     float acc = 0.f;
-    if (col < ncol)
-        for (int r = threadIdx.y; r < ntiles; r += 8) acc += part[(long long)r * ncol + col];
+    if (col < ncol) {
+#pragma unroll 4
+        for (int r = threadIdx.y; r < ntiles; r += 32) acc += part[(long long)r * ncol + col];
+    }
     red[threadIdx.y][threadIdx.x] = acc;
     __syncthreads();
-    if (threadIdx.y == 0 && col < ncol) {
-#pragma unroll
-        for (int r = 1; r < 8; ++r) acc += red[r][threadIdx.x];
-        const int j = col / D, d = col % D;
+    acc = warp_sum(red[threadIdx.x][threadIdx.y]);   // a warp per column now
+    const int mine = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && mine < ncol) {
+        const int j = mine / D, d = mine % D;
         if (j < W)
             gw[(long long)d * W + j] = acc;
         else if (gb)
@@ -346,7 +422,7 @@ conv_bwd_state_kernel(const T* __restrict__ x, long long ldx, const float* __res
                       const float* __restrict__ bias, const T* __restrict__ s0, const float* __restrict__ gy,
                       const float* __restrict__ gsT, float* __restrict__ gs0, Seqs q, int D)
 {
-    constexpr int V = kBwdV;
+    constexpr int V = kV;
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     const int i = blockIdx.x;
     if (c >= D) return;
@@ -395,19 +471,22 @@ conv_bwd_state_kernel(const T* __restrict__ x, long long ldx, const float* __res
 // ---------------------------------------------------------------- launches
 static int conv_threads(int vecs) { return vecs >= 128 ? 128 : (vecs + 31) / 32 * 32; }
 
-static int conv_bwd_tile(long long tokens)
+// Tokens per tile of the backward pass: 64 where that leaves enough threads, less
+// halo and fewer partial sums; at least 16; at most about 4096 partial sums.
+static int conv_bwd_tile(long long tokens, int D)
 {
-    const long long r = (tokens + 4095) / 4096;   // at most about 4096 partial sums
-    return (int)(r < 64 ? 64 : r);
+    int r = 64;
+    while (r > 16 && (tokens / r) * (D / kV) < 148LL * 256) r /= 2;
+    while ((tokens + r - 1) / r > 4096) r *= 2;
+    return r;
 }
 
 template <typename T, typename TO, int W, bool SILU>
 static cudaError_t launch_conv_fwd(const ConvArgs& a, const void* s0, void* y, void* sT, cudaStream_t st)
 {
-    constexpr int V = 16 / sizeof(T);
     const Seqs q{a.cu, a.nseq, a.T, a.tokens};
-    const int nt = conv_threads(a.D / V);
-    const unsigned cb = (a.D / V + nt - 1) / nt;
+    const int nt = conv_threads(a.D / kV);
+    const unsigned cb = (a.D / kV + nt - 1) / nt;
     // Tokens per tile: long tiles re-read less halo, short ones give enough
     // threads; at least ~1024 threads per SM while a tile keeps 16 tokens.
     int R = 64;
@@ -428,13 +507,18 @@ static cudaError_t launch_conv_fwd(const ConvArgs& a, const void* s0, void* y, v
 template <typename T, typename TO, int W, bool SILU>
 static cudaError_t launch_conv_step(const ConvArgs& a, void* state, void* y, cudaStream_t st)
 {
-    constexpr int V = 16 / sizeof(T);
-    const int nt = conv_threads(a.D / V);
-    const unsigned cb = (a.D / V + nt - 1) / nt;
-    int RN = 4;
-    while (RN > 1 && (long long)a.nseq / RN * cb * nt < 148LL * 256) RN /= 2;
-    conv_step_kernel<T, TO, W, SILU><<<dim3((a.nseq + RN - 1) / RN, cb), nt, 0, st>>>(
-        static_cast<const T*>(a.x), a.ldx, a.w, a.bias, static_cast<T*>(state), static_cast<TO*>(y), a.nseq, a.D, RN);
+    const int nt = conv_threads(a.D / kV);
+    const unsigned cb = (a.D / kV + nt - 1) / nt;
+    auto go = [&](auto rn) {
+        constexpr int RN = decltype(rn)::value;
+        conv_step_kernel<T, TO, W, SILU, RN><<<dim3((a.nseq + RN - 1) / RN, cb), nt, 0, st>>>(
+            static_cast<const T*>(a.x), a.ldx, a.w, a.bias, static_cast<T*>(state), static_cast<TO*>(y), a.nseq, a.D);
+    };
+    // four sequences per thread share its weights once that leaves 512 threads per SM
+    if ((long long)a.nseq / 4 * cb * nt >= 148LL * 512)
+        go(std::integral_constant<int, 4>{});
+    else
+        go(std::integral_constant<int, 1>{});
     return cudaGetLastError();
 }
 
@@ -443,14 +527,14 @@ static cudaError_t launch_conv_bwd(const ConvArgs& a, const void* s0, const floa
                                    float* gw, float* gb, float* gs0, float* part, cudaStream_t st)
 {
     const Seqs q{a.cu, a.nseq, a.T, a.tokens};
-    const int nt = conv_threads(a.D / kBwdV);
-    const unsigned cb = (a.D / kBwdV + nt - 1) / nt;
-    const int R = conv_bwd_tile(a.tokens);
+    const int nt = conv_threads(a.D / kV);
+    const unsigned cb = (a.D / kV + nt - 1) / nt;
+    const int R = conv_bwd_tile(a.tokens, a.D);
     const long long ntiles = (a.tokens + R - 1) / R;
     if (cb > 65535u) return cudaErrorInvalidConfiguration;
     conv_bwd_kernel<T, W, SILU><<<dim3((unsigned)ntiles, cb), nt, 0, st>>>(
         static_cast<const T*>(a.x), a.ldx, a.w, a.bias, static_cast<const T*>(s0), gy, gsT, gx, part, q, a.D, R);
-    conv_bwd_reduce_kernel<<<((W + 1) * a.D + 31) / 32, dim3(32, 8), 0, st>>>(part, (int)ntiles, gw, gb, a.D, W);
+    conv_bwd_reduce_kernel<<<((W + 1) * a.D + 31) / 32, dim3(32, 32), 0, st>>>(part, (int)ntiles, gw, gb, a.D, W);
     if (gs0)
         conv_bwd_state_kernel<T, W, SILU><<<dim3(a.nseq, cb), nt, 0, st>>>(
             static_cast<const T*>(a.x), a.ldx, a.w, a.bias, static_cast<const T*>(s0), gy, gsT, gs0, q, a.D);
@@ -503,7 +587,7 @@ cudaError_t conv_step(const ConvArgs& a, void* state, void* y, kda_dtype o_dtype
 
 size_t conv_bwd_workspace(long long tokens, int D, int W)
 {
-    const int R = mixer::conv_bwd_tile(tokens);
+    const int R = mixer::conv_bwd_tile(tokens, D);
     return (size_t)((tokens + R - 1) / R) * (W + 1) * D * sizeof(float);
 }
 

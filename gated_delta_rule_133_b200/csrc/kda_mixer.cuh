@@ -127,6 +127,81 @@ __device__ __forceinline__ float silu_grad(float x)
     return fmaf(x * s, 1.f - s, s);
 }
 
+// Two fp32 values in one 64-bit register: the packed multiply-add does both in
+// one issue slot.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack(float a, float b)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(f32x2 v, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 silu2(float x, float y)
+{
+    const f32x2 v = pack(x, y);
+    float a, b;
+    unpack(mul2(v, pack(-kLog2e, -kLog2e)), a, b);
+    unpack(add2(pack(exp2_approx(a), exp2_approx(b)), pack(1.f, 1.f)), a, b);
+    return mul2(v, pack(rcp_approx(a), rcp_approx(b)));
+}
+
+// silu'(x) = s + x s (1 - s)
+__device__ __forceinline__ f32x2 silu_grad2(float x, float y)
+{
+    const f32x2 v = pack(x, y), one = pack(1.f, 1.f);
+    float a, b;
+    unpack(mul2(v, pack(-kLog2e, -kLog2e)), a, b);
+    unpack(add2(pack(exp2_approx(a), exp2_approx(b)), one), a, b);
+    const f32x2 s = pack(rcp_approx(a), rcp_approx(b));
+    return fma2(mul2(v, s), fma2(s, pack(-1.f, -1.f), one), s);
+}
+
+// Two or four consecutive elements as loaded, and as fp32.
+template <typename T> struct Raw;
+template <> struct Raw<float> { typedef float2 pair; typedef float4 quad; };
+template <> struct Raw<__nv_bfloat16> { typedef unsigned pair; typedef uint2 quad; };
+__device__ __forceinline__ float2 widen(float2 v) { return v; }
+__device__ __forceinline__ float2 widen(unsigned v)
+{
+    float2 r;
+    unpack2(v, r.x, r.y);
+    return r;
+}
+__device__ __forceinline__ void widen(const float4& v, f32x2 (&x)[2])
+{
+    x[0] = pack(v.x, v.y);
+    x[1] = pack(v.z, v.w);
+}
+__device__ __forceinline__ void widen(const uint2& v, f32x2 (&x)[2])
+{
+    const float2 a = widen(v.x), b = widen(v.y);
+    x[0] = pack(a.x, a.y);
+    x[1] = pack(b.x, b.y);
+}
+
 // The sequences of a call: nseq equal ones of T tokens (cu == nullptr), or
 // packed ones given by cu over `tokens` tokens.
 struct Seqs {
@@ -212,8 +287,7 @@ struct SsmArgs {
     kda_dtype dtype;
 };
 
-size_t ssm_fwd_workspace(int nseq, int T, long long tokens, int D, int N, int G, bool varlen);
-cudaError_t ssm_fwd(const SsmArgs& a, void* y, float* sT, kda_dtype o_dtype, void* ws, cudaStream_t s);
+cudaError_t ssm_fwd(const SsmArgs& a, void* y, float* sT, kda_dtype o_dtype, cudaStream_t s);
 cudaError_t ssm_step(const SsmArgs& a, float* state, void* y, kda_dtype o_dtype, cudaStream_t s);
 
 struct SsmGrads {

@@ -110,17 +110,14 @@ kda_status check_ssm(const kda::SsmArgs& a, const void* y, int mode)
     return a.tokens > 0x7fffffffLL ? KDA_ERR_UNSUPPORTED : KDA_OK;
 }
 
-kda_status ssm_fwd_call(const kda::SsmArgs& a, void* y, float* sT, kda_dtype o_dtype, int mode, bool varlen, void* ws,
-                        size_t ws_bytes, void* stream)
+kda_status ssm_fwd_call(const kda::SsmArgs& a, void* y, float* sT, kda_dtype o_dtype, int mode, void* stream)
 {
-    kda_status st = check_ssm(a, y, mode);
+    const kda_status st = check_ssm(a, y, mode);
     if (st != KDA_OK) return st;
     if (!valid_dtype(o_dtype) || !opt_aligned16(sT)) return KDA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.tokens == 0) return copy_state(a.s0, sT, (size_t)a.nseq * a.D * a.N, s);
-    st = check_workspace(ws, ws_bytes, kda::ssm_fwd_workspace(a.nseq, a.T, a.tokens, a.D, a.N, a.G, varlen));
-    if (st != KDA_OK) return st;
-    return from_cuda(kda::ssm_fwd(a, y, sT, o_dtype, ws, s));
+    return from_cuda(kda::ssm_fwd(a, y, sT, o_dtype, s));
 }
 
 kda_status ssm_bwd_call(const kda::SsmArgs& a, const kda::SsmGrads& g, int mode, bool varlen, void* ws, size_t ws_bytes,
@@ -221,47 +218,25 @@ kda_status kda_conv_bwd_workspace_size(long long tokens, int D, int W, size_t* b
 kda_status kda_ssm_fwd(const void* x, long long ldx, const void* dt, long long lddt, const float* A, const void* B_,
                        long long ldb, const void* C_, long long ldc, const float* skip, const void* z, long long ldz,
                        const float* dt_bias, const float* initial_state, void* y, float* final_state, int B, int T,
-                       int D, int S, int G, kda_dtype dtype, kda_dtype o_dtype, int mode, void* workspace,
-                       size_t workspace_bytes_, void* stream)
+                       int D, int S, int G, kda_dtype dtype, kda_dtype o_dtype, int mode, void* stream)
 {
     if (B < 0 || T < 0) return KDA_ERR_INVALID_ARG;
     const kda::SsmArgs a{x, dt, B_, C_, z, ldx, lddt, ldb, ldc, ldz, A, skip, dt_bias, initial_state, nullptr, B, T,
                          (long long)B * T, D, S, G, (mode & KDA_SSM_SOFTPLUS) != 0, dtype};
-    return ssm_fwd_call(a, y, final_state, o_dtype, mode, false, workspace, workspace_bytes_, stream);
-}
-
-kda_status kda_ssm_fwd_workspace_size(int B, int T, int D, int S, int G, kda_dtype dtype, size_t* bytes)
-{
-    if (!bytes || B < 0 || T < 0) return KDA_ERR_INVALID_ARG;
-    const kda_status st = check_ssm_sizes(D, S, G, dtype);
-    if (st != KDA_OK) return st;
-    const long long tokens = (long long)B * T;
-    if (tokens > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-    *bytes = tokens == 0 ? 0 : kda::ssm_fwd_workspace(B, T, tokens, D, S, G, false);
-    return KDA_OK;
+    return ssm_fwd_call(a, y, final_state, o_dtype, mode, stream);
 }
 
 kda_status kda_ssm_varlen_fwd(const void* x, long long ldx, const void* dt, long long lddt, const float* A,
                               const void* B_, long long ldb, const void* C_, long long ldc, const float* skip,
                               const void* z, long long ldz, const float* dt_bias, const int32_t* cu_seqlens, int N,
                               const float* initial_state, void* y, float* final_state, int T, int D, int S, int G,
-                              kda_dtype dtype, kda_dtype o_dtype, int mode, void* workspace, size_t workspace_bytes_,
-                              void* stream)
+                              kda_dtype dtype, kda_dtype o_dtype, int mode, void* stream)
 {
     const kda_status st = check_cu(cu_seqlens, N, T);
     if (st != KDA_OK) return st;
     const kda::SsmArgs a{x, dt, B_, C_, z, ldx, lddt, ldb, ldc, ldz, A, skip, dt_bias, initial_state, cu_seqlens, N, T,
                          T, D, S, G, (mode & KDA_SSM_SOFTPLUS) != 0, dtype};
-    return ssm_fwd_call(a, y, final_state, o_dtype, mode, true, workspace, workspace_bytes_, stream);
-}
-
-kda_status kda_ssm_varlen_fwd_workspace_size(int N, int T, int D, int S, int G, kda_dtype dtype, size_t* bytes)
-{
-    if (!bytes || N < 0 || N > 65535 || T < 0) return KDA_ERR_INVALID_ARG;
-    const kda_status st = check_ssm_sizes(D, S, G, dtype);
-    if (st != KDA_OK) return st;
-    *bytes = (N == 0 || T == 0) ? 0 : kda::ssm_fwd_workspace(N, T, T, D, S, G, true);
-    return KDA_OK;
+    return ssm_fwd_call(a, y, final_state, o_dtype, mode, stream);
 }
 
 kda_status kda_ssm_step(const void* x, long long ldx, const void* dt, long long lddt, const float* A, const void* B_,

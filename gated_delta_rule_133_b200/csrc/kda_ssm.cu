@@ -216,48 +216,73 @@ ssm_walk_kernel(const SsmDev p, const WalkBwd wb)
 }
 
 // One token per sequence.  A lane owns 4 states (16 bytes) of a channel, a
-// thread the same 4 states of RN sequences, so that A is read once for them;
-// the state is read once and written once.
-template <typename T, int N>
+// thread the same 4 states of RN sequences, so that A is read once for them and
+// their states are in flight together; a state is read once and written once.
+// With RN = 4, what is per (sequence, channel) -- the step size, the gate, the
+// output -- is done by one lane for one of the four sequences instead of by
+// every lane for all of them.
+template <typename T, int N, int RN>
 __global__ void __launch_bounds__(256)
-ssm_step_kernel(const SsmDev p, int n_seq, int RN)
+ssm_step_kernel(const SsmDev p, int n_seq)
 {
+    static_assert(RN == 1 || RN == 4, "a row per lane of the smallest group, or one row");
     constexpr int L = N / 4;
-    const long long f = ((long long)blockIdx.x * 256 + threadIdx.x);   // float4 index within one sequence's state
-    const int d = (int)(f / L), l = (int)(f % L);
+    const int f = blockIdx.x * 256 + threadIdx.x;   // 16-byte vector within one sequence's state (D N / 4 < 2^24)
+    const int d = f / L, l = f % L;
     if (d >= p.D) return;   // D is a multiple of 8: whole groups of L <= 16 lanes leave together
     const unsigned mask = __activemask();
-    const int g = d / (p.D / p.G);
+    const int lane = threadIdx.x & 31, group = lane / L * L;
+    const int bn = d / (p.D / p.G) * N + 4 * l, i0 = blockIdx.y * RN;
+    float4* state = reinterpret_cast<float4*>(p.sT) + ((long long)i0 * p.D + d) * L + l;
+    const long long next = (long long)p.D * L;      // 16-byte vectors from sequence to sequence
+    const int rows = min(RN, n_seq - i0);
+    float4 h[RN];
+    float b[RN][4], c[RN][4];
+#pragma unroll
+    for (int r = 0; r < RN; ++r) {
+        if (r < rows) {
+            h[r] = state[r * next];
+            load_vec<4>(row<T>(p.b, i0 + r, p.ldb) + bn, b[r]);
+            load_vec<4>(row<T>(p.c, i0 + r, p.ldc) + bn, c[r]);
+        }
+    }
+    const int mine = RN == 1 ? 0 : l / (L / 4);     // the sequence whose elements are this lane's
+    float x = 0.f, delta = 0.f, z = 0.f;
+    if (mine < rows) {
+        x = Elem<T>::load(row<T>(p.x, i0 + mine, p.ldx) + d);
+        delta = Elem<T>::load(row<T>(p.dt, i0 + mine, p.lddt) + d);
+        if (p.z) z = Elem<T>::load(row<T>(p.z, i0 + mine, p.ldz) + d);
+    }
     float4 A = *reinterpret_cast<const float4*>(p.A + (long long)d * N + 4 * l);
     A.x *= kLog2e; A.y *= kLog2e; A.z *= kLog2e; A.w *= kLog2e;
-    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.skip ? p.skip[d] : 0.f;
-    const int i1 = min((int)(blockIdx.y + 1) * RN, n_seq);
-    for (int i = blockIdx.y * RN; i < i1; ++i) {
-        float4* sp = reinterpret_cast<float4*>(p.sT + ((long long)i * p.D + d) * N + 4 * l);
-        float4 h = *sp;
-        const float x = Elem<T>::load(row<T>(p.x, i, p.ldx) + d);
-        const float v = Elem<T>::load(row<T>(p.dt, i, p.lddt) + d) + bias;
-        float b[4], c[4];
-        load_vec<4>(row<T>(p.b, i, p.ldb) + g * N + 4 * l, b);
-        load_vec<4>(row<T>(p.c, i, p.ldc) + g * N + 4 * l, c);
-        const float delta = p.softplus ? softplus(v) : v, u = delta * x;
-        h.x = fmaf(exp2_approx(fmaf(delta, A.x, kDecayShift)), h.x, u * b[0]);
-        h.y = fmaf(exp2_approx(fmaf(delta, A.y, kDecayShift)), h.y, u * b[1]);
-        h.z = fmaf(exp2_approx(fmaf(delta, A.z, kDecayShift)), h.z, u * b[2]);
-        h.w = fmaf(exp2_approx(fmaf(delta, A.w, kDecayShift)), h.w, u * b[3]);
-        *sp = h;
-        float y = fmaf(c[0], h.x, c[1] * h.y) + fmaf(c[2], h.z, c[3] * h.w);
+    if (p.dt_bias) delta += p.dt_bias[d];
+    if (p.softplus) delta = softplus(delta);
+    const float u = delta * x;
+    float y[RN];
 #pragma unroll
-        for (int m = L / 2; m >= 1; m >>= 1) y += __shfl_xor_sync(mask, y, m);
-        if (l == 0) {
-            y = fmaf(skip, x, y);
-            if (p.z) y *= silu(Elem<T>::load(row<T>(p.z, i, p.ldz) + d));
-            const long long o = (long long)i * p.D + d;
-            if (p.o_bf16)
-                static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(y);
-            else
-                static_cast<float*>(p.y)[o] = y;
+    for (int r = 0; r < RN; ++r) {
+        const float dr = RN == 1 ? delta : __shfl_sync(mask, delta, group + r * (L / 4));
+        const float ur = RN == 1 ? u : __shfl_sync(mask, u, group + r * (L / 4));
+        y[r] = 0.f;
+        if (r < rows) {
+            h[r].x = fmaf(exp2_approx(fmaf(dr, A.x, kDecayShift)), h[r].x, ur * b[r][0]);
+            h[r].y = fmaf(exp2_approx(fmaf(dr, A.y, kDecayShift)), h[r].y, ur * b[r][1]);
+            h[r].z = fmaf(exp2_approx(fmaf(dr, A.z, kDecayShift)), h[r].z, ur * b[r][2]);
+            h[r].w = fmaf(exp2_approx(fmaf(dr, A.w, kDecayShift)), h[r].w, ur * b[r][3]);
+            state[r * next] = h[r];
+            y[r] = fmaf(c[r][0], h[r].x, c[r][1] * h[r].y) + fmaf(c[r][2], h[r].z, c[r][3] * h[r].w);
         }
+    }
+    reduce_transposed<RN, RN, L / RN>(y, lane, mask);
+#pragma unroll
+    for (int m = L / RN / 2; m >= 1; m >>= 1) y[0] += __shfl_xor_sync(mask, y[0], m);
+    if (l % (L / RN) == 0 && mine < rows) {
+        float out = p.skip ? fmaf(p.skip[d], x, y[0]) : y[0];
+        if (p.z) out *= silu(z);
+        if (p.o_bf16)
+            row<__nv_bfloat16>(p.y, i0 + mine, 2u * p.D)[d] = __float2bfloat16_rn(out);
+        else
+            row<float>(p.y, i0 + mine, 4u * p.D)[d] = out;
     }
 }
 
@@ -295,29 +320,32 @@ static cudaError_t walk_dispatch(const SsmArgs& a, const SsmDev& p, cudaStream_t
     return launch_walk<T, 64>(a, p, s);
 }
 
-template <typename T>
+template <typename T, int N>
 static cudaError_t launch_step(const SsmArgs& a, const SsmDev& p, cudaStream_t s)
 {
-    const long long vecs = (long long)a.D * (a.N / 4);
-    const unsigned gx = (unsigned)((vecs + 255) / 256);
-    int RN = 4;
-    while (RN > 1 && (long long)gx * a.nseq / RN < 148LL * 6) RN /= 2;
-    while ((a.nseq + RN - 1) / RN > 65535) RN *= 2;
-    const dim3 grid(gx, (a.nseq + RN - 1) / RN);
-    if (a.N == 16)
-        ssm_step_kernel<T, 16><<<grid, 256, 0, s>>>(p, a.nseq, RN);
-    else if (a.N == 32)
-        ssm_step_kernel<T, 32><<<grid, 256, 0, s>>>(p, a.nseq, RN);
-    else
-        ssm_step_kernel<T, 64><<<grid, 256, 0, s>>>(p, a.nseq, RN);
+    const unsigned gx = (unsigned)(((long long)a.D * (N / 4) + 255) / 256);
+    // four sequences per thread once that leaves 2048 threads per SM (or the grid's
+    // second dimension would run out)
+    if ((long long)gx * a.nseq / 4 >= 148LL * 8 || a.nseq > 65535) {
+        if ((a.nseq + 3) / 4 > 65535) return cudaErrorInvalidConfiguration;
+        ssm_step_kernel<T, N, 4><<<dim3(gx, (a.nseq + 3) / 4), 256, 0, s>>>(p, a.nseq);
+    } else {
+        ssm_step_kernel<T, N, 1><<<dim3(gx, a.nseq), 256, 0, s>>>(p, a.nseq);
+    }
     return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t step_dispatch(const SsmArgs& a, const SsmDev& p, cudaStream_t s)
+{
+    if (a.N == 16) return launch_step<T, 16>(a, p, s);
+    if (a.N == 32) return launch_step<T, 32>(a, p, s);
+    return launch_step<T, 64>(a, p, s);
 }
 
 }  // namespace mixer
 
-size_t ssm_fwd_workspace(int, int, long long, int, int, int, bool) { return 0; }
-
-cudaError_t ssm_fwd(const SsmArgs& a, void* y, float* sT, kda_dtype o_dtype, void*, cudaStream_t s)
+cudaError_t ssm_fwd(const SsmArgs& a, void* y, float* sT, kda_dtype o_dtype, cudaStream_t s)
 {
     const mixer::SsmDev p = mixer::ssm_dev(a, y, sT, o_dtype);
     return a.dtype == KDA_BF16 ? mixer::walk_dispatch<__nv_bfloat16>(a, p, s) : mixer::walk_dispatch<float>(a, p, s);
@@ -326,7 +354,7 @@ cudaError_t ssm_fwd(const SsmArgs& a, void* y, float* sT, kda_dtype o_dtype, voi
 cudaError_t ssm_step(const SsmArgs& a, float* state, void* y, kda_dtype o_dtype, cudaStream_t s)
 {
     const mixer::SsmDev p = mixer::ssm_dev(a, y, state, o_dtype);
-    return a.dtype == KDA_BF16 ? mixer::launch_step<__nv_bfloat16>(a, p, s) : mixer::launch_step<float>(a, p, s);
+    return a.dtype == KDA_BF16 ? mixer::step_dispatch<__nv_bfloat16>(a, p, s) : mixer::step_dispatch<float>(a, p, s);
 }
 
 }  // namespace kda

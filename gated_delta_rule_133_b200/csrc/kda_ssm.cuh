@@ -6,47 +6,6 @@
 namespace kda {
 namespace mixer {
 
-// Two fp32 values in one 64-bit register: the packed multiply-add does both in
-// one issue slot.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack(float a, float b)
-{
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack(f32x2 v, float& a, float& b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
-{
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
-{
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
-{
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ f32x2 silu2(float x, float y)
-{
-    const f32x2 v = pack(x, y);
-    float a, b;
-    unpack(mul2(v, pack(-kLog2e, -kLog2e)), a, b);
-    unpack(add2(pack(exp2_approx(a), exp2_approx(b)), pack(1.f, 1.f)), a, b);
-    return mul2(v, pack(rcp_approx(a), rcp_approx(b)));
-}
-
 // softplus(v) = max(v, 0) + log(1 + e), e = e^-|v|, of two values, to fp32 accuracy
 // for every v.  e: 2^(-|v| log2 e) with the rounding error of the exponent put back
 // (log2 e in two parts).  log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, without
@@ -94,7 +53,7 @@ __device__ __forceinline__ f32x2 decay2(f32x2 delta, f32x2 A2)
 // i V / LANES and on, in p[0 .. V / LANES).  V - V / LANES shuffles instead of
 // V log2(LANES).
 template <int V, int LANES, int STRIDE, int P>
-__device__ __forceinline__ void reduce_transposed(float (&p)[P], int lane)
+__device__ __forceinline__ void reduce_transposed(float (&p)[P], int lane, unsigned mask = 0xffffffffu)
 {
     static_assert(V <= P && V % LANES == 0, "values");
     if constexpr (LANES > 1) {
@@ -103,9 +62,9 @@ __device__ __forceinline__ void reduce_transposed(float (&p)[P], int lane)
         for (int j = 0; j < V / 2; ++j) {
             const float keep = up ? p[j + V / 2] : p[j];
             const float send = up ? p[j] : p[j + V / 2];
-            p[j] = keep + __shfl_xor_sync(0xffffffffu, send, STRIDE * LANES / 2);
+            p[j] = keep + __shfl_xor_sync(mask, send, STRIDE * LANES / 2);
         }
-        reduce_transposed<V / 2, LANES / 2, STRIDE>(p, lane);
+        reduce_transposed<V / 2, LANES / 2, STRIDE>(p, lane, mask);
     }
 }
 
@@ -128,18 +87,6 @@ template <typename E>
 __device__ __forceinline__ E* row(void* base, unsigned t, unsigned bytes)
 {
     return reinterpret_cast<E*>(static_cast<char*>(base) + (unsigned long long)t * bytes);
-}
-
-// Two channels, or four states of B or C, as loaded.
-template <typename T> struct Raw;
-template <> struct Raw<float> { typedef float2 pair; typedef float4 quad; };
-template <> struct Raw<__nv_bfloat16> { typedef unsigned pair; typedef uint2 quad; };
-__device__ __forceinline__ float2 widen(float2 v) { return v; }
-__device__ __forceinline__ float2 widen(unsigned v)
-{
-    float2 r;
-    unpack2(v, r.x, r.y);
-    return r;
 }
 
 // 2 P consecutive elements in shared memory, in pairs.  bf16 stays bf16 there: the

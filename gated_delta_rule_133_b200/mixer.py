@@ -17,7 +17,7 @@ device's current stream, and new tensors belong to that stream.
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 
 import torch
 
@@ -25,51 +25,46 @@ from . import _lib
 
 __all__ = ["kda_conv_fwd", "kda_conv_varlen_fwd", "kda_conv_step", "kda_conv_bwd", "kda_conv_varlen_bwd",
            "kda_ssm_fwd", "kda_ssm_varlen_fwd", "kda_ssm_step", "kda_ssm_bwd", "kda_ssm_varlen_bwd",
-           "conv_bwd_workspace_size", "ssm_fwd_workspace_size", "ssm_varlen_fwd_workspace_size",
-           "ssm_bwd_workspace_size", "ssm_varlen_bwd_workspace_size"]
+           "conv_bwd_workspace_size", "ssm_bwd_workspace_size", "ssm_varlen_bwd_workspace_size"]
 
 _DTYPES = {torch.float32: _lib.KDA_F32, torch.bfloat16: _lib.KDA_BF16}
 _F32 = torch.float32
 
 
-def _fail(name, what, got, want):
-    raise ValueError(f"{name} {what} {got}, expected {want}")
+# ------------------------------------------------------------------ arguments
+# A decode step's kernel takes a few microseconds, so the checks of a call are
+# written to pass quickly: one condition per tensor, the message only on failure.
+def _explain(t, name, shape, dtype, index):
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on CUDA device {index}")
 
 
-def _dense(t, name, shape, dtype, device):
-    """Pointer of a contiguous tensor (None for None)."""
+def _dense(t, name, shape, dtype, index):
+    """Pointer of a contiguous tensor on CUDA device `index` (None for None)."""
     if t is None:
         return None
-    if t.shape != shape:
-        _fail(name, "has shape", tuple(t.shape), tuple(shape))
-    if t.dtype != dtype:
-        _fail(name, "has dtype", t.dtype, dtype)
-    if t.device != device:
-        _fail(name, "is on", t.device, device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+        return t.data_ptr()
+    _explain(t, name, shape, dtype, index)
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(t, name, shape, lead, dtype, device):
+def _rows(t, name, shape, lead, dtype, index):
     """(pointer, row stride) of a token-major tensor whose first `lead`
     dimensions count tokens; the rest is one contiguous row."""
     if t is None:
         return None, 0
-    if t.shape != shape:
-        _fail(name, "has shape", tuple(t.shape), tuple(shape))
-    if t.dtype != dtype:
-        _fail(name, "has dtype", t.dtype, dtype)
-    if t.device != device:
-        _fail(name, "is on", t.device, device)
-    row = 1
-    for n in shape[lead:]:
-        row *= n
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _explain(t, name, shape, dtype, index)
+    row = shape[-1] if len(shape) == lead + 1 else shape[-1] * shape[-2]
     if t.is_contiguous():
         return t.data_ptr(), row
     stride = t.stride()
-    inner = 1
-    ok = True
+    inner, ok = 1, True
     for i in range(len(shape) - 1, lead - 1, -1):
         ok = ok and (shape[i] == 1 or stride[i] == inner)
         inner *= shape[i]
@@ -88,75 +83,100 @@ def _rows(t, name, shape, lead, dtype, device):
 
 
 def _types(x, o_dtype, y):
-    if x.dtype not in _DTYPES:
+    code = _DTYPES.get(x.dtype)
+    if code is None:
         raise ValueError(f"unsupported dtype {x.dtype}")
     o_dtype = y.dtype if y is not None else x.dtype if o_dtype is None else o_dtype
-    if o_dtype not in _DTYPES:
+    o_code = _DTYPES.get(o_dtype)
+    if o_code is None:
         raise ValueError(f"unsupported output dtype {o_dtype}")
-    return _DTYPES[x.dtype], o_dtype
+    return code, o_dtype, o_code
 
 
-def _lead(x, dims, name="x"):
+def _lead(x, dims):
     if x.dim() != dims:
-        _fail(name, "has", f"{x.dim()} dimensions", dims)
+        raise ValueError(f"x has {x.dim()} dimensions, expected {dims}")
     return x.shape
 
 
-@contextlib.contextmanager
-def _switched(device, stream):
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield stream.cuda_stream
+def _packed(cu_seqlens, x):
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected (N + 1,)")
+    _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, x.get_device())
+    return cu_seqlens.shape[0] - 1
 
 
-class _Current:
-    """The device's current stream, without switching anything."""
+class _on:
+    """Allocation and launches of a call: `stream`, or the current stream of CUDA
+    device `index`; gives its handle.  Nothing is switched where that is current
+    already."""
+    __slots__ = ("raw", "guards")
 
-    def __init__(self, device):
-        self.device = device
+    def __init__(self, index, stream):
+        if index < 0:
+            raise ValueError("the tensors are not on a CUDA device (there is no CPU path)")
+        self.guards = None
+        if stream is not None:
+            if stream.device.index != index:
+                raise ValueError(f"stream is on {stream.device}, the tensors on CUDA device {index}")
+            self.guards = (torch.cuda.device(index), torch.cuda.stream(stream))
+            self.raw = stream.cuda_stream
+        else:
+            if torch.cuda.current_device() != index:
+                self.guards = (torch.cuda.device(index),)
+            self.raw = torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
 
     def __enter__(self):
-        return torch.cuda.current_stream(self.device).cuda_stream
+        if self.guards:
+            for g in self.guards:
+                g.__enter__()
+        return self.raw
 
     def __exit__(self, *exc):
+        if self.guards:
+            for g in reversed(self.guards):
+                g.__exit__(*exc)
         return False
 
 
-def _on(device, stream):
-    """Context in which to allocate and launch; gives the raw stream."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors are on {device}, expected a CUDA device")
-    if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return _Current(device)
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, expected {device}")
-    return _switched(device, stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the same handle, without a Stream object
 
 
-def _scratch(nbytes, workspace, device):
+def _new(x, ld, dtype):
+    """New tensor of x's shape on its device (ld: x's row stride)."""
+    if dtype is x.dtype and ld == x.shape[-1]:   # x is contiguous: the cheapest allocation
+        return torch.empty_like(x)
+    return x.new_empty(x.shape, dtype=dtype)
+
+
+def _scratch(nbytes, workspace, x):
     if nbytes == 0:
         return None, 0, None
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        workspace = x.new_empty(nbytes, dtype=torch.uint8)
+    elif workspace.device != x.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
     return workspace.data_ptr(), workspace.numel(), workspace
+
+
+@functools.lru_cache(maxsize=None)
+def _entry(name):
+    return getattr(_lib.load(), name)
+
+
+def _call(name, *args):
+    status = _entry(name)(*args)
+    if status != _lib.KDA_OK:
+        raise _lib.KdaError(status, name)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def conv_bwd_workspace_size(tokens, D, W):
     """Workspace bytes of kda_conv_bwd / kda_conv_varlen_bwd for `tokens` tokens in all."""
     return _lib.workspace_size("kda_conv_bwd_workspace_size", tokens, D, W)
-
-
-def ssm_fwd_workspace_size(B, T, D, S, G=1, dtype=torch.bfloat16):
-    """Workspace bytes of kda_ssm_fwd."""
-    return _lib.workspace_size("kda_ssm_fwd_workspace_size", B, T, D, S, G, _DTYPES[dtype])
-
-
-def ssm_varlen_fwd_workspace_size(N, T, D, S, G=1, dtype=torch.bfloat16):
-    """Workspace bytes of kda_ssm_varlen_fwd for N packed sequences of T tokens in all."""
-    return _lib.workspace_size("kda_ssm_varlen_fwd_workspace_size", N, T, D, S, G, _DTYPES[dtype])
 
 
 def ssm_bwd_workspace_size(B, T, D, S, G=1, dtype=torch.bfloat16):
@@ -188,26 +208,19 @@ def kda_conv_varlen_fwd(x, weight, bias, cu_seqlens, initial_state=None, *, silu
     """kda_conv_fwd over N packed sequences: x [T, D], cu_seqlens [N + 1] int32
     on the device, states [N, W - 1, D]."""
     T, D = _lead(x, 2)
-    return _conv_fwd(x, weight, bias, cu_seqlens, _packed(cu_seqlens, x.device), T, initial_state, silu, y,
-                     final_state, output_final_state, o_dtype, stream)
-
-
-def _packed(cu_seqlens, device):
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        _fail("cu_seqlens", "has shape", tuple(cu_seqlens.shape), "(N + 1,)")
-    _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, device)
-    return cu_seqlens.shape[0] - 1
+    return _conv_fwd(x, weight, bias, cu_seqlens, _packed(cu_seqlens, x), T, initial_state, silu, y, final_state,
+                     output_final_state, o_dtype, stream)
 
 
 def _conv_params(weight, bias, D, dev):
     if weight.dim() != 2 or weight.shape[0] != D:
-        _fail("weight", "has shape", tuple(weight.shape), (D, "W"))
+        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected ({D}, W)")
     return (_dense(weight, "weight", weight.shape, _F32, dev), _dense(bias, "bias", (D,), _F32, dev), weight.shape[1])
 
 
 def _conv_fwd(x, weight, bias, cu, N, T, s0, silu, y, sT, want_state, o_dtype, stream):
-    dev, D = x.device, x.shape[-1]
-    code, o_dtype = _types(x, o_dtype, y)
+    dev, D = x.get_device(), x.shape[-1]
+    code, o_dtype, o_code = _types(x, o_dtype, y)
     xp, ldx = _rows(x, "x", x.shape, x.dim() - 1, x.dtype, dev)
     wp, bp, W = _conv_params(weight, bias, D, dev)
     s0p = _dense(s0, "initial_state", (N, W - 1, D), x.dtype, dev)
@@ -215,17 +228,17 @@ def _conv_fwd(x, weight, bias, cu, N, T, s0, silu, y, sT, want_state, o_dtype, s
     sTp = _dense(sT, "final_state", (N, W - 1, D), x.dtype, dev)
     with _on(dev, stream) as st:
         if y is None:
-            y = torch.empty(x.shape, dtype=o_dtype, device=dev)
+            y = _new(x, ldx, o_dtype)
             yp = y.data_ptr()
         if sT is None and want_state:
-            sT = torch.empty((N, W - 1, D), dtype=x.dtype, device=dev)
+            sT = x.new_empty((N, W - 1, D))
             sTp = sT.data_ptr()
-        tail = (s0p, yp, sTp) + ((N,) if cu is None else ()) + (T, D, W, code, _DTYPES[o_dtype],
-                                                                _lib.KDA_CONV_SILU if silu else 0, st)
+        mode = _lib.KDA_CONV_SILU if silu else 0
         if cu is None:
-            _lib.call("kda_conv_fwd", xp, ldx, wp, bp, *tail)
+            _call("kda_conv_fwd", xp, ldx, wp, bp, s0p, yp, sTp, N, T, D, W, code, o_code, mode, st)
         else:
-            _lib.call("kda_conv_varlen_fwd", xp, ldx, wp, bp, cu.data_ptr(), N, *tail)
+            _call("kda_conv_varlen_fwd", xp, ldx, wp, bp, cu.data_ptr(), N, s0p, yp, sTp, T, D, W, code, o_code, mode,
+                  st)
     return y, sT
 
 
@@ -233,18 +246,17 @@ def kda_conv_step(x, weight, bias, state, *, silu=True, y=None, o_dtype=None, st
     """One token per sequence: x [N, D]; state [N, W - 1, D] of x's dtype, moved on
     by one token in place.  Returns y [N, D]."""
     N, D = _lead(x, 2)
-    dev = x.device
-    code, o_dtype = _types(x, o_dtype, y)
+    dev = x.get_device()
+    code, o_dtype, o_code = _types(x, o_dtype, y)
     xp, ldx = _rows(x, "x", x.shape, 1, x.dtype, dev)
     wp, bp, W = _conv_params(weight, bias, D, dev)
     sp = _dense(state, "state", (N, W - 1, D), x.dtype, dev)
     yp = _dense(y, "y", x.shape, o_dtype, dev)
     with _on(dev, stream) as st:
         if y is None:
-            y = torch.empty(x.shape, dtype=o_dtype, device=dev)
+            y = _new(x, ldx, o_dtype)
             yp = y.data_ptr()
-        _lib.call("kda_conv_step", xp, ldx, wp, bp, sp, yp, N, D, W, code, _DTYPES[o_dtype],
-                  _lib.KDA_CONV_SILU if silu else 0, st)
+        _call("kda_conv_step", xp, ldx, wp, bp, sp, yp, N, D, W, code, o_code, _lib.KDA_CONV_SILU if silu else 0, st)
     return y
 
 
@@ -263,13 +275,13 @@ def kda_conv_varlen_bwd(x, weight, bias, cu_seqlens, initial_state, grad_y, grad
                         want_initial_state_grad=True, stream=None, workspace=None):
     """Backward of kda_conv_varlen_fwd (x, grad_y [T, D], states [N, W - 1, D])."""
     T, D = _lead(x, 2)
-    return _conv_bwd(x, weight, bias, cu_seqlens, _packed(cu_seqlens, x.device), T, initial_state, grad_y,
-                     grad_final_state, silu, want_initial_state_grad, stream, workspace)
+    return _conv_bwd(x, weight, bias, cu_seqlens, _packed(cu_seqlens, x), T, initial_state, grad_y, grad_final_state,
+                     silu, want_initial_state_grad, stream, workspace)
 
 
 def _conv_bwd(x, weight, bias, cu, N, T, s0, gy, gsT, silu, want_gs0, stream, workspace):
-    dev, D = x.device, x.shape[-1]
-    code, _ = _types(x, None, None)
+    dev, D = x.get_device(), x.shape[-1]
+    code = _types(x, None, None)[0]
     xp, ldx = _rows(x, "x", x.shape, x.dim() - 1, x.dtype, dev)
     wp, bp, W = _conv_params(weight, bias, D, dev)
     s0p = _dense(s0, "initial_state", (N, W - 1, D), x.dtype, dev)
@@ -277,41 +289,40 @@ def _conv_bwd(x, weight, bias, cu, N, T, s0, gy, gsT, silu, want_gs0, stream, wo
     gsTp = _dense(gsT, "grad_final_state", (N, W - 1, D), _F32, dev)
     nbytes = conv_bwd_workspace_size(T if cu is not None else N * T, D, W)
     with _on(dev, stream) as st:
-        f32 = dict(dtype=_F32, device=dev)
-        gx, gw = torch.empty(x.shape, **f32), torch.empty((D, W), **f32)
-        gb = torch.empty(D, **f32) if bias is not None else None
-        gs0 = torch.empty((N, W - 1, D), **f32) if want_gs0 else None
-        ws, n, _keep = _scratch(nbytes, workspace, dev)
-        tail = (s0p, gyp, gsTp, gx.data_ptr(), gw.data_ptr(), None if gb is None else gb.data_ptr(),
-                None if gs0 is None else gs0.data_ptr()) + ((N,) if cu is None else ()) + (
-                    T, D, W, code, _lib.KDA_CONV_SILU if silu else 0, ws, n, st)
+        gx, gw = x.new_empty(x.shape, dtype=_F32), torch.empty_like(weight)
+        gb = torch.empty_like(bias) if bias is not None else None
+        gs0 = x.new_empty((N, W - 1, D), dtype=_F32) if want_gs0 else None
+        ws, n, _keep = _scratch(nbytes, workspace, x)
+        grads = (gx.data_ptr(), gw.data_ptr(), _ptr(gb), _ptr(gs0))
+        mode = _lib.KDA_CONV_SILU if silu else 0
         if cu is None:
-            _lib.call("kda_conv_bwd", xp, ldx, wp, bp, *tail)
+            _call("kda_conv_bwd", xp, ldx, wp, bp, s0p, gyp, gsTp, *grads, N, T, D, W, code, mode, ws, n, st)
         else:
-            _lib.call("kda_conv_varlen_bwd", xp, ldx, wp, bp, cu.data_ptr(), N, *tail)
+            _call("kda_conv_varlen_bwd", xp, ldx, wp, bp, cu.data_ptr(), N, s0p, gyp, gsTp, *grads, T, D, W, code, mode,
+                  ws, n, st)
     return gx, gw, gb, gs0
 
 
 # ------------------------------------------------------------------ selective scan
 def _ssm_in(x, dt, A, B, C, skip, z, dt_bias):
     """Checked (pointers and row strides in the C ABI's order, S, G)."""
-    dev, D, lead = x.device, x.shape[-1], x.dim() - 1
+    dev, shape, lead, ty = x.get_device(), x.shape, x.dim() - 1, x.dtype
+    D = shape[-1]
     if A.dim() != 2 or A.shape[0] != D:
-        _fail("A", "has shape", tuple(A.shape), (D, "S"))
+        raise ValueError(f"A has shape {tuple(A.shape)}, expected ({D}, S)")
     S = A.shape[1]
     if B.dim() != lead + 2:
-        _fail("B", "has", f"{B.dim()} dimensions", lead + 2)
+        raise ValueError(f"B has {B.dim()} dimensions, expected {lead + 2}")
     G = B.shape[lead]
-    bc = x.shape[:lead] + (G, S)
-    ty = x.dtype
+    bc = shape[:lead] + (G, S)
     skp, dbp = _dense(skip, "skip", (D,), _F32, dev), _dense(dt_bias, "dt_bias", (D,), _F32, dev)
-    return (*_rows(x, "x", x.shape, lead, ty, dev), *_rows(dt, "dt", x.shape, lead, ty, dev),
+    return (*_rows(x, "x", shape, lead, ty, dev), *_rows(dt, "dt", shape, lead, ty, dev),
             _dense(A, "A", A.shape, _F32, dev), *_rows(B, "B", bc, lead, ty, dev), *_rows(C, "C", bc, lead, ty, dev),
-            skp, *_rows(z, "z", x.shape, lead, ty, dev), dbp), S, G
+            skp, *_rows(z, "z", shape, lead, ty, dev), dbp), S, G
 
 
 def kda_ssm_fwd(x, dt, A, B, C, skip=None, z=None, dt_bias=None, initial_state=None, *, softplus=True, y=None,
-                final_state=None, output_final_state=True, o_dtype=None, stream=None, workspace=None):
+                final_state=None, output_final_state=True, o_dtype=None, stream=None):
     """Selective scan over equal-length sequences.
 
     x, dt, z [B, T, D] and B, C [B, T, G, S] (bf16 or fp32); A [D, S], skip and
@@ -320,42 +331,37 @@ def kda_ssm_fwd(x, dt, A, B, C, skip=None, z=None, dt_bias=None, initial_state=N
     (y [B, T, D] in o_dtype, by default x's dtype; final_state [B, D, S] or None)."""
     N, T, _ = _lead(x, 3)
     return _ssm_fwd(x, dt, A, B, C, None, N, T, skip, z, dt_bias, initial_state, softplus, y, final_state,
-                    output_final_state, o_dtype, stream, workspace)
+                    output_final_state, o_dtype, stream)
 
 
 def kda_ssm_varlen_fwd(x, dt, A, B, C, cu_seqlens, skip=None, z=None, dt_bias=None, initial_state=None, *,
-                       softplus=True, y=None, final_state=None, output_final_state=True, o_dtype=None, stream=None,
-                       workspace=None):
+                       softplus=True, y=None, final_state=None, output_final_state=True, o_dtype=None, stream=None):
     """kda_ssm_fwd over N packed sequences: x, dt, z [T, D], B, C [T, G, S],
     cu_seqlens [N + 1] int32 on the device, states [N, D, S]."""
     T, _ = _lead(x, 2)
-    return _ssm_fwd(x, dt, A, B, C, cu_seqlens, _packed(cu_seqlens, x.device), T, skip, z, dt_bias, initial_state,
-                    softplus, y, final_state, output_final_state, o_dtype, stream, workspace)
+    return _ssm_fwd(x, dt, A, B, C, cu_seqlens, _packed(cu_seqlens, x), T, skip, z, dt_bias, initial_state, softplus,
+                    y, final_state, output_final_state, o_dtype, stream)
 
 
-def _ssm_fwd(x, dt, A, B, C, cu, N, T, skip, z, dt_bias, s0, softplus, y, sT, want_state, o_dtype, stream, workspace):
-    dev, D = x.device, x.shape[-1]
-    code, o_dtype = _types(x, o_dtype, y)
+def _ssm_fwd(x, dt, A, B, C, cu, N, T, skip, z, dt_bias, s0, softplus, y, sT, want_state, o_dtype, stream):
+    dev, D = x.get_device(), x.shape[-1]
+    code, o_dtype, o_code = _types(x, o_dtype, y)
     ins, S, G = _ssm_in(x, dt, A, B, C, skip, z, dt_bias)
     s0p = _dense(s0, "initial_state", (N, D, S), _F32, dev)
     yp = _dense(y, "y", x.shape, o_dtype, dev)
     sTp = _dense(sT, "final_state", (N, D, S), _F32, dev)
-    nbytes = _lib.workspace_size("kda_ssm_fwd_workspace_size" if cu is None else "kda_ssm_varlen_fwd_workspace_size",
-                                 N, T, D, S, G, code)
     with _on(dev, stream) as st:
         if y is None:
-            y = torch.empty(x.shape, dtype=o_dtype, device=dev)
+            y = _new(x, ins[1], o_dtype)
             yp = y.data_ptr()
         if sT is None and want_state:
-            sT = torch.empty((N, D, S), dtype=_F32, device=dev)
+            sT = x.new_empty((N, D, S), dtype=_F32)
             sTp = sT.data_ptr()
-        ws, n, _keep = _scratch(nbytes, workspace, dev)
-        tail = (s0p, yp, sTp) + ((N,) if cu is None else ()) + (T, D, S, G, code, _DTYPES[o_dtype],
-                                                                _lib.KDA_SSM_SOFTPLUS if softplus else 0, ws, n, st)
+        mode = _lib.KDA_SSM_SOFTPLUS if softplus else 0
         if cu is None:
-            _lib.call("kda_ssm_fwd", *ins, *tail)
+            _call("kda_ssm_fwd", *ins, s0p, yp, sTp, N, T, D, S, G, code, o_code, mode, st)
         else:
-            _lib.call("kda_ssm_varlen_fwd", *ins, cu.data_ptr(), N, *tail)
+            _call("kda_ssm_varlen_fwd", *ins, cu.data_ptr(), N, s0p, yp, sTp, T, D, S, G, code, o_code, mode, st)
     return y, sT
 
 
@@ -364,17 +370,16 @@ def kda_ssm_step(x, dt, A, B, C, state, skip=None, z=None, dt_bias=None, *, soft
     """One token per sequence: x, dt, z [N, D], B, C [N, G, S]; state [N, D, S] fp32
     updated in place.  Returns y [N, D]."""
     N, D = _lead(x, 2)
-    dev = x.device
-    code, o_dtype = _types(x, o_dtype, y)
+    dev = x.get_device()
+    code, o_dtype, o_code = _types(x, o_dtype, y)
     ins, S, G = _ssm_in(x, dt, A, B, C, skip, z, dt_bias)
     sp = _dense(state, "state", (N, D, S), _F32, dev)
     yp = _dense(y, "y", x.shape, o_dtype, dev)
     with _on(dev, stream) as st:
         if y is None:
-            y = torch.empty(x.shape, dtype=o_dtype, device=dev)
+            y = _new(x, ins[1], o_dtype)
             yp = y.data_ptr()
-        _lib.call("kda_ssm_step", *ins, sp, yp, N, D, S, G, code, _DTYPES[o_dtype],
-                  _lib.KDA_SSM_SOFTPLUS if softplus else 0, st)
+        _call("kda_ssm_step", *ins, sp, yp, N, D, S, G, code, o_code, _lib.KDA_SSM_SOFTPLUS if softplus else 0, st)
     return y
 
 
@@ -395,13 +400,13 @@ def kda_ssm_varlen_bwd(x, dt, A, B, C, cu_seqlens, skip, z, dt_bias, initial_sta
                        softplus=True, want_initial_state_grad=True, stream=None, workspace=None):
     """Backward of kda_ssm_varlen_fwd (packed layouts, states [N, D, S])."""
     T, _ = _lead(x, 2)
-    return _ssm_bwd(x, dt, A, B, C, cu_seqlens, _packed(cu_seqlens, x.device), T, skip, z, dt_bias, initial_state,
-                    grad_y, grad_final_state, softplus, want_initial_state_grad, stream, workspace)
+    return _ssm_bwd(x, dt, A, B, C, cu_seqlens, _packed(cu_seqlens, x), T, skip, z, dt_bias, initial_state, grad_y,
+                    grad_final_state, softplus, want_initial_state_grad, stream, workspace)
 
 
 def _ssm_bwd(x, dt, A, B, C, cu, N, T, skip, z, dt_bias, s0, gy, gsT, softplus, want_gs0, stream, workspace):
-    dev, D = x.device, x.shape[-1]
-    code, _ = _types(x, None, None)
+    dev, D = x.get_device(), x.shape[-1]
+    code = _types(x, None, None)[0]
     ins, S, G = _ssm_in(x, dt, A, B, C, skip, z, dt_bias)
     s0p = _dense(s0, "initial_state", (N, D, S), _F32, dev)
     gyp = _dense(gy, "grad_y", x.shape, _F32, dev)
@@ -409,19 +414,19 @@ def _ssm_bwd(x, dt, A, B, C, cu, N, T, skip, z, dt_bias, s0, gy, gsT, softplus, 
     nbytes = _lib.workspace_size("kda_ssm_bwd_workspace_size" if cu is None else "kda_ssm_varlen_bwd_workspace_size",
                                  N, T, D, S, G, code)
     with _on(dev, stream) as st:
-        f32 = dict(dtype=_F32, device=dev)
-        gx, gdt, gA = torch.empty(x.shape, **f32), torch.empty(x.shape, **f32), torch.empty((D, S), **f32)
-        gB, gC = torch.empty(B.shape, **f32), torch.empty(C.shape, **f32)
-        gskip = torch.empty(D, **f32) if skip is not None else None
-        gz = torch.empty(x.shape, **f32) if z is not None else None
-        gbias = torch.empty(D, **f32) if dt_bias is not None else None
-        gs0 = torch.empty((N, D, S), **f32) if want_gs0 else None
-        ws, n, _keep = _scratch(nbytes, workspace, dev)
+        f32 = dict(dtype=_F32)
+        gx, gdt, gA = x.new_empty(x.shape, **f32), x.new_empty(x.shape, **f32), torch.empty_like(A)
+        gB, gC = x.new_empty(B.shape, **f32), x.new_empty(C.shape, **f32)
+        gskip = torch.empty_like(skip) if skip is not None else None
+        gz = x.new_empty(x.shape, **f32) if z is not None else None
+        gbias = torch.empty_like(dt_bias) if dt_bias is not None else None
+        gs0 = x.new_empty((N, D, S), **f32) if want_gs0 else None
+        ws, n, _keep = _scratch(nbytes, workspace, x)
         grads = (gx, gdt, gA, gB, gC, gskip, gz, gbias, gs0)
-        tail = (s0p, gyp, gsTp, *(None if g is None else g.data_ptr() for g in grads)) + (
-            (N,) if cu is None else ()) + (T, D, S, G, code, _lib.KDA_SSM_SOFTPLUS if softplus else 0, ws, n, st)
+        mode = _lib.KDA_SSM_SOFTPLUS if softplus else 0
         if cu is None:
-            _lib.call("kda_ssm_bwd", *ins, *tail)
+            _call("kda_ssm_bwd", *ins, s0p, gyp, gsTp, *map(_ptr, grads), N, T, D, S, G, code, mode, ws, n, st)
         else:
-            _lib.call("kda_ssm_varlen_bwd", *ins, cu.data_ptr(), N, *tail)
+            _call("kda_ssm_varlen_bwd", *ins, cu.data_ptr(), N, s0p, gyp, gsTp, *map(_ptr, grads), T, D, S, G, code,
+                  mode, ws, n, st)
     return grads

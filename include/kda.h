@@ -370,8 +370,8 @@ kda_status kda_dplr_varlen_fwd_workspace_size(int N, int T, int H, int dk, int d
  * state is zero.  fp32 arithmetic; y is rounded once, to o_dtype.
  *
  *   x        rows of D elements of type `dtype`, row (b, t) at x + (b T + t) ldx:
- *            ldx >= D elements, a multiple of 16 bytes (D for a dense tensor),
- *            so x may be a column slice of a wider projection
+ *            ldx >= D elements, a multiple of 16 bytes, below 2^30 (D for a dense
+ *            tensor), so x may be a column slice of a wider projection
  *   weight   [D, W] fp32; bias [D] fp32 or NULL; 16-byte aligned
  *   initial_state / final_state [N, W - 1, D] of type `dtype` or NULL (final may
  *            be the same memory as initial); copies of inputs, never rounded
@@ -438,18 +438,16 @@ kda_status kda_conv_bwd_workspace_size(long long tokens, int D, int W, size_t* b
  *
  *   x, dt, z   rows of D elements, B, C rows of G * S elements, all of type
  *              `dtype`; row (b, t) at pointer + (b T + t) * its ld, ld in elements,
- *              a multiple of 16 bytes, at least the row's length
+ *              a multiple of 16 bytes, at least the row's length, below 2^30
  *   A          [D, S] fp32, <= 0 (not checked); skip, dt_bias [D] fp32 or NULL
  *   initial_state / final_state [N, D, S] fp32 or NULL (final may be the same
  *              memory as initial)
  *   y          [B, T, D] (dense) or [T, D] (packed), o_dtype, written
  *   mode       0 or KDA_SSM_SOFTPLUS
- *   workspace  at least the *_workspace_size() bytes, 256-byte aligned, contents
- *              need no initialisation; NULL when that size is 0
  * D a multiple of 8 * G, at most 2^20, S in {16, 32, 64}: others return
  * KDA_ERR_UNSUPPORTED.  Pointers 16-byte aligned.  Packed batches follow
  * kda_varlen_fwd's rules (skipped sequences: y rows not written, final state =
- * initial state; rows of no sequence not written).
+ * initial state; rows of no sequence not written).  Needs no workspace.
  */
 #define KDA_SSM_SOFTPLUS 1
 
@@ -457,19 +455,13 @@ kda_status kda_ssm_fwd(const void* x, long long ldx, const void* dt, long long l
                        const void* B_, long long ldb, const void* C_, long long ldc, const float* skip,
                        const void* z, long long ldz, const float* dt_bias, const float* initial_state,
                        void* y, float* final_state, int B, int T, int D, int S, int G,
-                       kda_dtype dtype, kda_dtype o_dtype, int mode, void* workspace, size_t workspace_bytes,
-                       void* stream);
-
-kda_status kda_ssm_fwd_workspace_size(int B, int T, int D, int S, int G, kda_dtype dtype, size_t* bytes);
+                       kda_dtype dtype, kda_dtype o_dtype, int mode, void* stream);
 
 kda_status kda_ssm_varlen_fwd(const void* x, long long ldx, const void* dt, long long lddt, const float* A,
                               const void* B_, long long ldb, const void* C_, long long ldc, const float* skip,
                               const void* z, long long ldz, const float* dt_bias, const int32_t* cu_seqlens, int N,
                               const float* initial_state, void* y, float* final_state, int T, int D, int S, int G,
-                              kda_dtype dtype, kda_dtype o_dtype, int mode, void* workspace,
-                              size_t workspace_bytes, void* stream);
-
-kda_status kda_ssm_varlen_fwd_workspace_size(int N, int T, int D, int S, int G, kda_dtype dtype, size_t* bytes);
+                              kda_dtype dtype, kda_dtype o_dtype, int mode, void* stream);
 
 /* One token for each of N sequences (rows n of x, dt, B, C, z; y [N, D]);
  * state [N, D, S] fp32 updated in place.  Memory bound: the state is read once
@@ -487,6 +479,9 @@ kda_status kda_ssm_step(const void* x, long long ldx, const void* dt, long long 
  *   grad_skip [D], grad_z [B, T, D], grad_dt_bias [D] fp32: written, and required,
  *              where skip, z, dt_bias are given; NULL where they are not
  *   grad_initial_state [B, D, S] fp32, or NULL if not wanted
+ *   workspace  at least kda_ssm_bwd_workspace_size() bytes, 256-byte aligned,
+ *              contents need no initialisation (a state for every 4 or 8 tokens,
+ *              partial sums)
  * Sums over tokens, channels and sequences are added in a fixed order.  Packed
  * batches: gradient rows of no sequence and of skipped ones are zero, a skipped
  * sequence's grad_initial_state is grad_final_state.  The gradient buffers must
