@@ -237,13 +237,10 @@ ssm_step_kernel(const SsmDev p, int n_seq)
     const long long next = (long long)p.D * L;      // 16-byte vectors from sequence to sequence
     const int rows = min(RN, n_seq - i0);
     float4 h[RN];
-    float b[RN][4], c[RN][4];
 #pragma unroll
     for (int r = 0; r < RN; ++r) {
         if (r < rows) {
-            h[r] = state[r * next];
-            load_vec<4>(row<T>(p.b, i0 + r, p.ldb) + bn, b[r]);
-            load_vec<4>(row<T>(p.c, i0 + r, p.ldc) + bn, c[r]);
+            h[r] = __ldcs(state + r * next);
         }
     }
     const int mine = RN == 1 ? 0 : l / (L / 4);     // the sequence whose elements are this lane's
@@ -265,12 +262,15 @@ ssm_step_kernel(const SsmDev p, int n_seq)
         const float ur = RN == 1 ? u : __shfl_sync(mask, u, group + r * (L / 4));
         y[r] = 0.f;
         if (r < rows) {
-            h[r].x = fmaf(exp2_approx(fmaf(dr, A.x, kDecayShift)), h[r].x, ur * b[r][0]);
-            h[r].y = fmaf(exp2_approx(fmaf(dr, A.y, kDecayShift)), h[r].y, ur * b[r][1]);
-            h[r].z = fmaf(exp2_approx(fmaf(dr, A.z, kDecayShift)), h[r].z, ur * b[r][2]);
-            h[r].w = fmaf(exp2_approx(fmaf(dr, A.w, kDecayShift)), h[r].w, ur * b[r][3]);
-            state[r * next] = h[r];
-            y[r] = fmaf(c[r][0], h[r].x, c[r][1] * h[r].y) + fmaf(c[r][2], h[r].z, c[r][3] * h[r].w);
+            float b[4], c[4];   // read here: held from the start they would halve the blocks per SM
+            load_vec<4>(row<T>(p.b, i0 + r, p.ldb) + bn, b);
+            load_vec<4>(row<T>(p.c, i0 + r, p.ldc) + bn, c);
+            h[r].x = fmaf(exp2_approx(fmaf(dr, A.x, kDecayShift)), h[r].x, ur * b[0]);
+            h[r].y = fmaf(exp2_approx(fmaf(dr, A.y, kDecayShift)), h[r].y, ur * b[1]);
+            h[r].z = fmaf(exp2_approx(fmaf(dr, A.z, kDecayShift)), h[r].z, ur * b[2]);
+            h[r].w = fmaf(exp2_approx(fmaf(dr, A.w, kDecayShift)), h[r].w, ur * b[3]);
+            __stcs(state + r * next, h[r]);
+            y[r] = fmaf(c[0], h[r].x, c[1] * h[r].y) + fmaf(c[2], h[r].z, c[3] * h[r].w);
         }
     }
     reduce_transposed<RN, RN, L / RN>(y, lane, mask);

@@ -4,9 +4,10 @@
 //   w_t = g_t a_t h_{t-1},   dA = sum_t w_t Delta_t,   dDelta_t = sum_n w_t A + du_t x_t
 //   dx_t = du_t Delta_t + skip dy0_t,   ddt_t = dDelta_t sigmoid(dt_t + bias)
 //   dz_t = gy_t y0_t silu'(z_t),   dh_0 = a_0 g_0
-// Four launches: the forward walk, which leaves the state before every CK-th
-// token (and dz, as it has y0); the reverse walk, which recomputes CK states at
-// a time into registers and runs the reverse recurrence over them; and two sums
+// Four launches: the forward walk, which leaves the state before every CK-th token
+// and forms dz where it has y0 anyway;
+// the reverse walk, which recomputes CK states at a time into registers and runs
+// the reverse recurrence over them; and two sums
 // in a fixed order, of dB and dC over channel tiles and of dA, dskip and dbias
 // over the blocks that share a channel.
 #include "kda_sm100.cuh"
@@ -33,23 +34,109 @@ struct BwdDev {
 template <int N_>
 struct Rev {
     static constexpr int N = N_, L = N == 16 ? 4 : 8, NPT = N / L, DT = 32 / L, TK = 32 / NPT, TILE = 32;
-    static constexpr int SETS = TILE / DT, W = N == 64 ? 8 : 12, THREADS = 32 * W;
-    static constexpr int V = 2 * NPT, VL = V / DT;          // values of dB, dC per token: of a lane, left to a lane
+    static constexpr int SETS = TILE / DT, W = N == 16 ? 12 : 8, THREADS = 32 * W;
+    static constexpr int VL = 2 * NPT / DT;                 // values of dB, dC of a token left to a lane
     static constexpr int EL = TK * DT / 2;                  // lanes with a pair of channels outside the walk
-    static constexpr int DUROW = DT + 2, DYROW = DT + 2, BQ = TK * N / 128;
+    static constexpr int DUROW = DT + 2, DYROW = DT + 2, SROW = 2 * DT, BQ = TK * N / 128;
+    static constexpr int COPY = TK * N + (N == 64 ? 0 : N);   // elements from order to order of B, C: on other banks
     // floats of shared memory: per warp, and in all
     template <typename T>
     static constexpr int warp_floats()
     {
-        return TK * (2 * DUROW + DYROW + 2 * DT) + 2 * TK * N * (int)sizeof(T) / 4;
+        return TK * (2 * DUROW + DYROW + SROW) + 2 * 4 * COPY * (int)sizeof(T) / 4;
     }
     template <typename T>
     static constexpr size_t smem()
     {
         return 4 * ((size_t)W * warp_floats<T>() + SETS * 32 * NPT + 2 * (size_t)W * SETS * 32 * NPT +
-                    (size_t)W * SETS * EL * 4) + 8 * W * SETS + 16;
+                    (size_t)W * SETS * EL * 4 + 2 * TILE) + 8 * W * SETS + 16;
     }
 };
+
+// The order of a lane's states.  The sums of dB and dC over a warp's channels
+// halve the values at every step: a lane sends one half and keeps the other, and
+// which half depends on its channel.  So that no value has to be selected, a lane
+// holds state i ^ X of its NPT in place i, X from the bits of its channel: what it
+// keeps is always in front.  (B and C are staged in four orders for that.)
+template <int N>
+struct Order {
+    using K = Rev<N>;
+    static constexpr int HI = K::NPT / 2;                           // the step between lanes 16 apart swaps halves
+    static constexpr int LO = K::NPT / 4 ? (N == 16 ? 1 : K::NPT / 4) : 1;
+    static constexpr int LOBIT = N == 16 ? 2 : 3;                   // the last step's lane bit
+    __device__ __forceinline__ static int copy(int lane) { return (lane >> 4 & 1) * 2 + (lane >> LOBIT & 1); }
+    __device__ __forceinline__ static constexpr int x_of(int copy) { return (copy >> 1) * HI + (copy & 1) * LO; }
+};
+
+// A quad of B or C with its elements in places ^ X (X's two low bits).
+__device__ __forceinline__ uint2 permuted(const uint2& v, int X)
+{
+    uint2 r = (X & 2) ? make_uint2(v.y, v.x) : v;
+    if (X & 1) r = make_uint2(__byte_perm(r.x, 0u, 0x1032), __byte_perm(r.y, 0u, 0x1032));
+    return r;
+}
+__device__ __forceinline__ float4 permuted(const float4& v, int X)
+{
+    float4 r = (X & 2) ? make_float4(v.z, v.w, v.x, v.y) : v;
+    if (X & 1) r = make_float4(r.y, r.x, r.w, r.z);
+    return r;
+}
+
+// A lane's states in global memory (natural order), in its own order.
+template <int P>
+__device__ __forceinline__ void read_permuted(const float* p, f32x2 (&v)[P], int X)
+{
+#pragma unroll
+    for (int n = 0; n < P; ++n) {
+        const float2 f = *reinterpret_cast<const float2*>(p + 2 * (n ^ (X >> 1)));
+        v[n] = (X & 1) ? pack(f.y, f.x) : pack(f.x, f.y);
+    }
+}
+template <int P>
+__device__ __forceinline__ void write_permuted(float* p, const f32x2 (&v)[P], int X)
+{
+#pragma unroll
+    for (int n = 0; n < P; ++n) {
+        float a, b;
+        unpack(v[n], a, b);
+        *reinterpret_cast<float2*>(p + 2 * (n ^ (X >> 1))) = (X & 1) ? make_float2(b, a) : make_float2(a, b);
+    }
+}
+
+__device__ __forceinline__ f32x2 add_shuffled(f32x2 keep, f32x2 send, int mask)
+{
+    return add2(keep, __shfl_xor_sync(0xffffffffu, send, mask));
+}
+
+// One token's dB (vb) and dC (vc) summed over the warp's channels; acc gets what is
+// left to the lane: N = 16: one state of dB or (lane bit 3) dC; N = 32: one state of
+// both; N = 64: two states of both.
+__device__ __forceinline__ void sum_channels(const f32x2 (&vb)[2], const f32x2 (&vc)[2], int lane, float (&acc)[1])
+{
+    const f32x2 kb = add_shuffled(vb[0], vb[1], 16), kc = add_shuffled(vc[0], vc[1], 16);
+    const bool up = lane & 8;
+    float lo, hi;
+    unpack(add_shuffled(up ? kc : kb, up ? kb : kc, 8), lo, hi);
+    acc[0] += lo + __shfl_xor_sync(0xffffffffu, hi, 4);
+}
+__device__ __forceinline__ void sum_channels(const f32x2 (&vb)[2], const f32x2 (&vc)[2], int, float (&acc)[2])
+{
+    float lo, hi;
+    unpack(add_shuffled(vb[0], vb[1], 16), lo, hi);
+    acc[0] += lo + __shfl_xor_sync(0xffffffffu, hi, 8);
+    unpack(add_shuffled(vc[0], vc[1], 16), lo, hi);
+    acc[1] += lo + __shfl_xor_sync(0xffffffffu, hi, 8);
+}
+__device__ __forceinline__ void sum_channels(const f32x2 (&vb)[4], const f32x2 (&vc)[4], int, float (&acc)[4])
+{
+    float lo, hi;
+    unpack(add_shuffled(add_shuffled(vb[0], vb[2], 16), add_shuffled(vb[1], vb[3], 16), 8), lo, hi);
+    acc[0] += lo;
+    acc[1] += hi;
+    unpack(add_shuffled(add_shuffled(vc[0], vc[2], 16), add_shuffled(vc[1], vc[3], 16), 8), lo, hi);
+    acc[2] += lo;
+    acc[3] += hi;
+}
 
 // As in the forward walk, the warps of a block take turns, backwards in time: a
 // warp recomputes the states of its TK tokens from the checkpoint before them,
@@ -71,14 +158,17 @@ ssm_reverse_kernel(const BwdDev b)
     float* sCarry = sA + SETS * 32 * NPT;                                // [warp][set][lane][NPT]
     float* sGA = sCarry + W * SETS * 32 * NPT;                           // the same: sums of dA
     float* sGP = sGA + W * SETS * 32 * NPT;                              // [warp][set][EL][4]: dskip, dbias of a pair
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sGP + W * SETS * K::EL * 4);   // [warp][set]
+    float* sBias = sGP + W * SETS * K::EL * 4;                           // [channel of the tile]
+    float* sSkip = sBias + K::TILE;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sSkip + K::TILE);       // [warp][set]
     int* aborted = reinterpret_cast<int*>(bars + W * SETS);
     float* mine = base + w * K::template warp_floats<T>();
     float2* sDU = reinterpret_cast<float2*>(mine);                       // [token][channel]: Delta, u
     float* sDY = mine + 2 * TK * K::DUROW;                               // [token][channel]: dy0
     float* sS = sDY + TK * K::DYROW;                                     // [token][channel][2]: sums of g B, w A
-    T* sB = reinterpret_cast<T*>(sS + 2 * TK * DT);                      // [token][N]
-    T* sC = sB + TK * N;
+    T* sB = reinterpret_cast<T*>(sS + TK * K::SROW);                     // [order][token][N]
+    T* sC = sB + 4 * K::COPY;
+    const int copy = Order<N>::copy(lane), X = Order<N>::x_of(copy);
 
     flag_bad_sequences(p.q);
     const int ntiles = p.tiles * p.G;
@@ -87,11 +177,17 @@ ssm_reverse_kernel(const BwdDev b)
     const int sets = min(SETS, (Dg - off) / DT);   // D / G is a multiple of 8: whole sets
 
     for (int i = threadIdx.x; i < SETS * 32 * NPT; i += K::THREADS) {
-        const int ch = i / N;   // [set][channel][N] is the same order as [set][lane][NPT]
-        sA[i] = ch < sets * DT ? p.A[(long long)(c00 + ch) * N + i % N] : 0.f;
+        // [set][lane][place]
+        const int ch = i / N, of = i / NPT % 32, n = i % N ^ Order<N>::x_of(Order<N>::copy(of));
+        sA[i] = ch < sets * DT ? p.A[(long long)(c00 + ch) * N + n] : 0.f;
     }
     for (int i = threadIdx.x; i < W * SETS * 32 * NPT; i += K::THREADS) sGA[i] = 0.f;
     for (int i = threadIdx.x; i < W * SETS * K::EL * 4; i += K::THREADS) sGP[i] = 0.f;
+    if (threadIdx.x < K::TILE) {
+        const bool in = (int)threadIdx.x < sets * DT;
+        sBias[threadIdx.x] = in && p.dt_bias ? p.dt_bias[c00 + threadIdx.x] : 0.f;
+        sSkip[threadIdx.x] = in && p.skip ? p.skip[c00 + threadIdx.x] : 0.f;
+    }
     if (threadIdx.x < W * SETS) sm100::mbar_init(bars + threadIdx.x, 1);
     if (threadIdx.x == 0) {
         *aborted = 0;
@@ -123,7 +219,7 @@ ssm_reverse_kernel(const BwdDev b)
 
         Pair nx, ndt, nz;
         float2 ngy;
-        f32x2 nh[NPT / 2];
+        float2 nh[NPT / 2];
         auto fetch = [&](int blk, int o) {   // set o of block blk (blk < 0: none left)
             nx = ndt = nz = Pair{};
             ngy = make_float2(0.f, 0.f);
@@ -137,7 +233,8 @@ ssm_reverse_kernel(const BwdDev b)
                 ngy = *reinterpret_cast<const float2*>(row<float>(b.gy, t, 4u * p.D) + ch);
             }
             const float* cp = b.ckpt + ((ckpt0 + blk) * p.D + c00 + o * DT) * N + lane * NPT;
-            read_states(cp, nh);
+#pragma unroll
+            for (int n = 0; n < NPT / 2; ++n) nh[n] = *reinterpret_cast<const float2*>(cp + 2 * (n ^ (X >> 1)));
         };
         if (w < nb) fetch(nb - 1 - w, 0);
 
@@ -152,8 +249,12 @@ ssm_reverse_kernel(const BwdDev b)
                     vb = *reinterpret_cast<const Quad*>(row<T>(p.b, first + t, p.ldb) + n);
                     vc = *reinterpret_cast<const Quad*>(row<T>(p.c, first + t, p.ldc) + n);
                 }
-                reinterpret_cast<Quad*>(sB)[i] = vb;
-                reinterpret_cast<Quad*>(sC)[i] = vc;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int Xk = Order<N>::x_of(k), at = k * (K::COPY / 4) + (i ^ (Xk >> 2));
+                    reinterpret_cast<Quad*>(sB)[at] = permuted(vb, Xk);
+                    reinterpret_cast<Quad*>(sC)[at] = permuted(vc, Xk);
+                }
             }
             float acc[TK][VL];
 #pragma unroll
@@ -164,9 +265,9 @@ ssm_reverse_kernel(const BwdDev b)
             for (int o = 0; o < sets; ++o) {
                 // the pair's elements
                 const float2 x = widen(nx), z = widen(nz), raw = widen(ndt);
-                float2 dy = ngy, v = raw, bias = make_float2(0.f, 0.f), delta;
+                float2 dy = ngy, v = raw, delta;
+                const float2 bias = *reinterpret_cast<const float2*>(sBias + o * DT + ec);
                 const int ch = c00 + o * DT + ec;
-                if (p.dt_bias && el) bias = *reinterpret_cast<const float2*>(p.dt_bias + ch);
                 v.x += bias.x;
                 v.y += bias.y;
                 delta = v;
@@ -178,7 +279,7 @@ ssm_reverse_kernel(const BwdDev b)
                 }
                 f32x2 h0[NPT / 2];
 #pragma unroll
-                for (int n = 0; n < NPT / 2; ++n) h0[n] = nh[n];
+                for (int n = 0; n < NPT / 2; ++n) h0[n] = (X & 1) ? pack(nh[n].y, nh[n].x) : pack(nh[n].x, nh[n].y);
                 if (el) {
                     *reinterpret_cast<float4*>(&sDU[et * K::DUROW + ec]) =
                         make_float4(delta.x, delta.x * x.x, delta.y, delta.y * x.y);
@@ -194,8 +295,8 @@ ssm_reverse_kernel(const BwdDev b)
                     const float2 du = sDU[j * K::DUROW + c];
                     const float d = sDY[j * K::DYROW + c];
                     f32x2 B[NPT / 2], C[NPT / 2];
-                    read_states(sB + j * N + l * NPT, B);
-                    read_states(sC + j * N + l * NPT, C);
+                    read_states(sB + copy * K::COPY + j * N + l * NPT, B);
+                    read_states(sC + copy * K::COPY + j * N + l * NPT, C);
 #pragma unroll
                     for (int n = 0; n < NPT / 2; ++n) {
                         a[j][n] = decay2(pack(du.x, du.x), mul2(A[n], pack(kLog2e, kLog2e)));
@@ -210,8 +311,8 @@ ssm_reverse_kernel(const BwdDev b)
                     read_states(sCarry + ((from * SETS + o) * 32 + lane) * NPT, cr);
                 } else {
 #pragma unroll
-                    for (int n = 0; n < NPT / 2; ++n)
-                        cr[n] = b.gsT ? *reinterpret_cast<const f32x2*>(b.gsT + srow + o * 32 * NPT + 2 * n) : 0ull;
+                    for (int n = 0; n < NPT / 2; ++n) cr[n] = 0ull;
+                    if (b.gsT) read_permuted(b.gsT + srow + o * 32 * NPT, cr, X);
                 }
                 // q becomes g, and a the gradient handed to the token before: a g
 #pragma unroll
@@ -226,8 +327,7 @@ ssm_reverse_kernel(const BwdDev b)
                     __syncwarp();
                     if (lane == 0) sm100::mbar_arrive(bars + w * SETS + o);
                 } else if (b.gs0) {
-#pragma unroll
-                    for (int n = 0; n < NPT / 2; ++n) *reinterpret_cast<f32x2*>(b.gs0 + srow + o * 32 * NPT + 2 * n) = cr[n];
+                    write_permuted(b.gs0 + srow + o * 32 * NPT, cr, X);
                 }
 
                 f32x2 gA[NPT / 2];
@@ -241,21 +341,18 @@ ssm_reverse_kernel(const BwdDev b)
                         const int j = jg + jj;
                         const float2 du = sDU[j * K::DUROW + c];
                         const float d = sDY[j * K::DYROW + c];
-                        f32x2 B[NPT / 2], s1 = 0ull, s2 = 0ull;
-                        read_states(sB + j * N + l * NPT, B);
-                        float val[K::V];
+                        f32x2 B[NPT / 2], vb[NPT / 2], vc[NPT / 2], s1 = 0ull, s2 = 0ull;
+                        read_states(sB + copy * K::COPY + j * N + l * NPT, B);
 #pragma unroll
                         for (int n = 0; n < NPT / 2; ++n) {
-                            unpack(mul2(q[j][n], pack(du.y, du.y)), val[2 * n], val[2 * n + 1]);
-                            unpack(mul2(h[j][n], pack(d, d)), val[NPT + 2 * n], val[NPT + 2 * n + 1]);
+                            vb[n] = mul2(q[j][n], pack(du.y, du.y));
+                            vc[n] = mul2(h[j][n], pack(d, d));
                             s1 = n ? fma2(q[j][n], B[n], s1) : mul2(q[j][n], B[n]);
                             const f32x2 wt = mul2(a[j][n], j ? h[j > 0 ? j - 1 : 0][n] : h0[n]);
                             gA[n] = fma2(wt, pack(du.x, du.x), gA[n]);
                             s2 = n ? fma2(wt, A[n], s2) : mul2(wt, A[n]);
                         }
-                        reduce_transposed<K::V, DT, L>(val, lane);
-#pragma unroll
-                        for (int k = 0; k < VL; ++k) acc[j][k] += val[k];
+                        sum_channels(vb, vc, lane, acc[j]);
                         float lo, hi;
                         unpack(s1, lo, hi);
                         sums[2 * jj] = lo + hi;
@@ -268,9 +365,8 @@ ssm_reverse_kernel(const BwdDev b)
                 write_states(sGA + ((w * SETS + o) * 32 + lane) * NPT, gA);
                 __syncwarp();
                 if (el && t0 + et < len) {
-                    const float4 ss = *reinterpret_cast<const float4*>(sS + (et * DT + ec) * 2);   // s1, s2 of both channels
-                    float2 skip = make_float2(0.f, 0.f);
-                    if (p.skip) skip = *reinterpret_cast<const float2*>(p.skip + ch);
+                    const float4 ss = *reinterpret_cast<const float4*>(sS + (et * DT + ec) * 2);   // of both channels
+                    const float2 skip = *reinterpret_cast<const float2*>(sSkip + o * DT + ec);
                     const unsigned t = first + t0 + et;
                     float2 gx, gd;
                     gx.x = fmaf(ss.x, delta.x, skip.x * dy.x);
@@ -291,14 +387,21 @@ ssm_reverse_kernel(const BwdDev b)
             }
             if (!ok) break;
             if (r > 0) parity ^= 1u;
-            // dB, dC of the tile's channels: values i0 .. of (dB, dC) x NPT states
-            const int i0 = lane / L * VL, col = i0 / NPT * N + l * NPT + i0 % NPT;
+            // dB, dC of the tile's channels
+            const int n = l * NPT + X;
 #pragma unroll
             for (int j = 0; j < TK; ++j) {
                 if (t0 + j < len) {
-                    float* o = b.part + (((long long)gt * p.q.tokens + first + t0 + j) * p.G + g) * 2 * N + col;
-#pragma unroll
-                    for (int k = 0; k < VL; ++k) o[k] = acc[j][k];
+                    float* o = b.part + (((long long)gt * p.q.tokens + first + t0 + j) * p.G + g) * 2 * N + n;
+                    if constexpr (N == 16) {
+                        o[(lane >> 3 & 1) * N] = acc[j][0];
+                    } else if constexpr (N == 32) {
+                        o[0] = acc[j][0];
+                        o[N] = acc[j][1];
+                    } else {
+                        *reinterpret_cast<float2*>(o) = make_float2(acc[j][0], acc[j][1]);
+                        *reinterpret_cast<float2*>(o + N) = make_float2(acc[j][2], acc[j][3]);
+                    }
                 }
             }
         }
@@ -309,7 +412,8 @@ ssm_reverse_kernel(const BwdDev b)
     for (int i = threadIdx.x; i < sets * 32 * NPT; i += K::THREADS) {
         float sum = 0.f;
         for (int v = 0; v < W; ++v) sum += sGA[v * SETS * 32 * NPT + i];
-        b.partA[((long long)slot * p.D + c00) * N + i] = sum;
+        const int n = i % N ^ Order<N>::x_of(Order<N>::copy(i / NPT % 32));
+        b.partA[((long long)slot * p.D + c00 + i / N) * N + n] = sum;
     }
     for (int i = threadIdx.x; i < sets * DT * 2; i += K::THREADS) {
         const int ch = i / 2, which = i % 2, o = ch / DT, cc = ch % DT;

@@ -164,10 +164,8 @@ def _entry(name):
     return getattr(_lib.load(), name)
 
 
-def _call(name, *args):
-    status = _entry(name)(*args)
-    if status != _lib.KDA_OK:
-        raise _lib.KdaError(status, name)
+def _raise(status, name):
+    raise _lib.KdaError(status, name)
 
 
 def _ptr(t):
@@ -235,10 +233,14 @@ def _conv_fwd(x, weight, bias, cu, N, T, s0, silu, y, sT, want_state, o_dtype, s
             sTp = sT.data_ptr()
         mode = _lib.KDA_CONV_SILU if silu else 0
         if cu is None:
-            _call("kda_conv_fwd", xp, ldx, wp, bp, s0p, yp, sTp, N, T, D, W, code, o_code, mode, st)
+            status = _entry("kda_conv_fwd")(xp, ldx, wp, bp, s0p, yp, sTp, N, T, D, W, code, o_code, mode, st)
+            if status:
+                _raise(status, "kda_conv_fwd")
         else:
-            _call("kda_conv_varlen_fwd", xp, ldx, wp, bp, cu.data_ptr(), N, s0p, yp, sTp, T, D, W, code, o_code, mode,
-                  st)
+            status = _entry("kda_conv_varlen_fwd")(
+                xp, ldx, wp, bp, cu.data_ptr(), N, s0p, yp, sTp, T, D, W, code, o_code, mode, st)
+            if status:
+                _raise(status, "kda_conv_varlen_fwd")
     return y, sT
 
 
@@ -256,7 +258,10 @@ def kda_conv_step(x, weight, bias, state, *, silu=True, y=None, o_dtype=None, st
         if y is None:
             y = _new(x, ldx, o_dtype)
             yp = y.data_ptr()
-        _call("kda_conv_step", xp, ldx, wp, bp, sp, yp, N, D, W, code, o_code, _lib.KDA_CONV_SILU if silu else 0, st)
+        status = _entry("kda_conv_step")(
+            xp, ldx, wp, bp, sp, yp, N, D, W, code, o_code, _lib.KDA_CONV_SILU if silu else 0, st)
+        if status:
+            _raise(status, "kda_conv_step")
     return y
 
 
@@ -296,10 +301,14 @@ def _conv_bwd(x, weight, bias, cu, N, T, s0, gy, gsT, silu, want_gs0, stream, wo
         grads = (gx.data_ptr(), gw.data_ptr(), _ptr(gb), _ptr(gs0))
         mode = _lib.KDA_CONV_SILU if silu else 0
         if cu is None:
-            _call("kda_conv_bwd", xp, ldx, wp, bp, s0p, gyp, gsTp, *grads, N, T, D, W, code, mode, ws, n, st)
+            status = _entry("kda_conv_bwd")(xp, ldx, wp, bp, s0p, gyp, gsTp, *grads, N, T, D, W, code, mode, ws, n, st)
+            if status:
+                _raise(status, "kda_conv_bwd")
         else:
-            _call("kda_conv_varlen_bwd", xp, ldx, wp, bp, cu.data_ptr(), N, s0p, gyp, gsTp, *grads, T, D, W, code, mode,
-                  ws, n, st)
+            status = _entry("kda_conv_varlen_bwd")(
+                xp, ldx, wp, bp, cu.data_ptr(), N, s0p, gyp, gsTp, *grads, T, D, W, code, mode, ws, n, st)
+            if status:
+                _raise(status, "kda_conv_varlen_bwd")
     return gx, gw, gb, gs0
 
 
@@ -315,6 +324,16 @@ def _ssm_in(x, dt, A, B, C, skip, z, dt_bias):
         raise ValueError(f"B has {B.dim()} dimensions, expected {lead + 2}")
     G = B.shape[lead]
     bc = shape[:lead] + (G, S)
+    if (x.is_contiguous() and dt.dtype is ty and dt.shape == shape and dt.is_contiguous() and dt.get_device() == dev
+            and A.dtype is _F32 and A.is_contiguous() and A.get_device() == dev
+            and B.dtype is ty and B.shape == bc and B.is_contiguous() and B.get_device() == dev
+            and C.dtype is ty and C.shape == bc and C.is_contiguous() and C.get_device() == dev
+            and (z is None or (z.dtype is ty and z.shape == shape and z.is_contiguous() and z.get_device() == dev))):
+        # everything dense: the common call, and the cheapest way through
+        row = G * S
+        return (x.data_ptr(), D, dt.data_ptr(), D, A.data_ptr(), B.data_ptr(), row, C.data_ptr(), row,
+                _dense(skip, "skip", (D,), _F32, dev), None if z is None else z.data_ptr(), D,
+                _dense(dt_bias, "dt_bias", (D,), _F32, dev)), S, G
     skp, dbp = _dense(skip, "skip", (D,), _F32, dev), _dense(dt_bias, "dt_bias", (D,), _F32, dev)
     return (*_rows(x, "x", shape, lead, ty, dev), *_rows(dt, "dt", shape, lead, ty, dev),
             _dense(A, "A", A.shape, _F32, dev), *_rows(B, "B", bc, lead, ty, dev), *_rows(C, "C", bc, lead, ty, dev),
@@ -359,9 +378,14 @@ def _ssm_fwd(x, dt, A, B, C, cu, N, T, skip, z, dt_bias, s0, softplus, y, sT, wa
             sTp = sT.data_ptr()
         mode = _lib.KDA_SSM_SOFTPLUS if softplus else 0
         if cu is None:
-            _call("kda_ssm_fwd", *ins, s0p, yp, sTp, N, T, D, S, G, code, o_code, mode, st)
+            status = _entry("kda_ssm_fwd")(*ins, s0p, yp, sTp, N, T, D, S, G, code, o_code, mode, st)
+            if status:
+                _raise(status, "kda_ssm_fwd")
         else:
-            _call("kda_ssm_varlen_fwd", *ins, cu.data_ptr(), N, s0p, yp, sTp, T, D, S, G, code, o_code, mode, st)
+            status = _entry("kda_ssm_varlen_fwd")(
+                *ins, cu.data_ptr(), N, s0p, yp, sTp, T, D, S, G, code, o_code, mode, st)
+            if status:
+                _raise(status, "kda_ssm_varlen_fwd")
     return y, sT
 
 
@@ -379,7 +403,10 @@ def kda_ssm_step(x, dt, A, B, C, state, skip=None, z=None, dt_bias=None, *, soft
         if y is None:
             y = _new(x, ins[1], o_dtype)
             yp = y.data_ptr()
-        _call("kda_ssm_step", *ins, sp, yp, N, D, S, G, code, o_code, _lib.KDA_SSM_SOFTPLUS if softplus else 0, st)
+        status = _entry("kda_ssm_step")(
+            *ins, sp, yp, N, D, S, G, code, o_code, _lib.KDA_SSM_SOFTPLUS if softplus else 0, st)
+        if status:
+            _raise(status, "kda_ssm_step")
     return y
 
 
@@ -425,8 +452,13 @@ def _ssm_bwd(x, dt, A, B, C, cu, N, T, skip, z, dt_bias, s0, gy, gsT, softplus, 
         grads = (gx, gdt, gA, gB, gC, gskip, gz, gbias, gs0)
         mode = _lib.KDA_SSM_SOFTPLUS if softplus else 0
         if cu is None:
-            _call("kda_ssm_bwd", *ins, s0p, gyp, gsTp, *map(_ptr, grads), N, T, D, S, G, code, mode, ws, n, st)
+            status = _entry("kda_ssm_bwd")(
+                *ins, s0p, gyp, gsTp, *map(_ptr, grads), N, T, D, S, G, code, mode, ws, n, st)
+            if status:
+                _raise(status, "kda_ssm_bwd")
         else:
-            _call("kda_ssm_varlen_bwd", *ins, cu.data_ptr(), N, s0p, gyp, gsTp, *map(_ptr, grads), T, D, S, G, code,
-                  mode, ws, n, st)
+            status = _entry("kda_ssm_varlen_bwd")(
+                *ins, cu.data_ptr(), N, s0p, gyp, gsTp, *map(_ptr, grads), T, D, S, G, code, mode, ws, n, st)
+            if status:
+                _raise(status, "kda_ssm_varlen_bwd")
     return grads
