@@ -106,40 +106,43 @@ def _packed(cu_seqlens, x):
     return cu_seqlens.shape[0] - 1
 
 
-class _on:
-    """Allocation and launches of a call: `stream`, or the current stream of CUDA
-    device `index`; gives its handle.  Nothing is switched where that is current
-    already."""
-    __slots__ = ("raw", "guards")
+_current = torch.cuda.current_device
+
+
+class _switched:
+    """Makes `stream` (or CUDA device `index`) current for a call that names another one."""
+    __slots__ = ("guards",)
 
     def __init__(self, index, stream):
         if index < 0:
             raise ValueError("the tensors are not on a CUDA device (there is no CPU path)")
-        self.guards = None
+        self.guards = (torch.cuda.device(index),)
         if stream is not None:
             if stream.device.index != index:
                 raise ValueError(f"stream is on {stream.device}, the tensors on CUDA device {index}")
-            self.guards = (torch.cuda.device(index), torch.cuda.stream(stream))
-            self.raw = stream.cuda_stream
-        else:
-            if torch.cuda.current_device() != index:
-                self.guards = (torch.cuda.device(index),)
-            self.raw = torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
+            self.guards += (torch.cuda.stream(stream),)
 
     def __enter__(self):
-        if self.guards:
-            for g in self.guards:
-                g.__enter__()
-        return self.raw
+        for g in self.guards:
+            g.__enter__()
 
     def __exit__(self, *exc):
-        if self.guards:
-            for g in reversed(self.guards):
-                g.__exit__(*exc)
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
         return False
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the same handle, without a Stream object
+def _elsewhere(index, stream):
+    """Whether a call has to switch first: to a stream of its own, or to its
+    tensors' device.  (A CPU tensor's index is -1: refused by _switched.)"""
+    return stream is not None or index < 0 or _current() != index
+
+
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)   # the handle without a Stream object
 
 
 def _new(x, ld, dtype):
@@ -211,9 +214,11 @@ def kda_conv_varlen_fwd(x, weight, bias, cu_seqlens, initial_state=None, *, silu
 
 
 def _conv_params(weight, bias, D, dev):
-    if weight.dim() != 2 or weight.shape[0] != D:
-        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected ({D}, W)")
-    return (_dense(weight, "weight", weight.shape, _F32, dev), _dense(bias, "bias", (D,), _F32, dev), weight.shape[1])
+    shape = weight.shape
+    if len(shape) != 2 or shape[0] != D:
+        raise ValueError(f"weight has shape {tuple(shape)}, expected ({D}, W)")
+    return (_dense(weight, "weight", shape, _F32, dev),
+            None if bias is None else _dense(bias, "bias", (D,), _F32, dev), shape[1])
 
 
 def _conv_fwd(x, weight, bias, cu, N, T, s0, silu, y, sT, want_state, o_dtype, stream):
@@ -224,23 +229,26 @@ def _conv_fwd(x, weight, bias, cu, N, T, s0, silu, y, sT, want_state, o_dtype, s
     s0p = _dense(s0, "initial_state", (N, W - 1, D), x.dtype, dev)
     yp = _dense(y, "y", x.shape, o_dtype, dev)
     sTp = _dense(sT, "final_state", (N, W - 1, D), x.dtype, dev)
-    with _on(dev, stream) as st:
-        if y is None:
-            y = _new(x, ldx, o_dtype)
-            yp = y.data_ptr()
-        if sT is None and want_state:
-            sT = x.new_empty((N, W - 1, D))
-            sTp = sT.data_ptr()
-        mode = _lib.KDA_CONV_SILU if silu else 0
-        if cu is None:
-            status = _entry("kda_conv_fwd")(xp, ldx, wp, bp, s0p, yp, sTp, N, T, D, W, code, o_code, mode, st)
-            if status:
-                _raise(status, "kda_conv_fwd")
-        else:
-            status = _entry("kda_conv_varlen_fwd")(
-                xp, ldx, wp, bp, cu.data_ptr(), N, s0p, yp, sTp, T, D, W, code, o_code, mode, st)
-            if status:
-                _raise(status, "kda_conv_varlen_fwd")
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return _conv_fwd(x, weight, bias, cu, N, T, s0, silu, y, sT, want_state, o_dtype, None)
+    st = _raw_stream(dev)
+    if y is None:
+        y = _new(x, ldx, o_dtype)
+        yp = y.data_ptr()
+    if sT is None and want_state:
+        sT = torch.empty_like(s0) if s0 is not None else x.new_empty((N, W - 1, D))
+        sTp = sT.data_ptr()
+    mode = _lib.KDA_CONV_SILU if silu else 0
+    if cu is None:
+        status = _entry("kda_conv_fwd")(xp, ldx, wp, bp, s0p, yp, sTp, N, T, D, W, code, o_code, mode, st)
+        if status:
+            _raise(status, "kda_conv_fwd")
+    else:
+        status = _entry("kda_conv_varlen_fwd")(
+            xp, ldx, wp, bp, cu.data_ptr(), N, s0p, yp, sTp, T, D, W, code, o_code, mode, st)
+        if status:
+            _raise(status, "kda_conv_varlen_fwd")
     return y, sT
 
 
@@ -254,14 +262,17 @@ def kda_conv_step(x, weight, bias, state, *, silu=True, y=None, o_dtype=None, st
     wp, bp, W = _conv_params(weight, bias, D, dev)
     sp = _dense(state, "state", (N, W - 1, D), x.dtype, dev)
     yp = _dense(y, "y", x.shape, o_dtype, dev)
-    with _on(dev, stream) as st:
-        if y is None:
-            y = _new(x, ldx, o_dtype)
-            yp = y.data_ptr()
-        status = _entry("kda_conv_step")(
-            xp, ldx, wp, bp, sp, yp, N, D, W, code, o_code, _lib.KDA_CONV_SILU if silu else 0, st)
-        if status:
-            _raise(status, "kda_conv_step")
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return kda_conv_step(x, weight, bias, state, silu=silu, y=y, o_dtype=o_dtype)
+    st = _raw_stream(dev)
+    if y is None:
+        y = _new(x, ldx, o_dtype)
+        yp = y.data_ptr()
+    status = _entry("kda_conv_step")(
+        xp, ldx, wp, bp, sp, yp, N, D, W, code, o_code, _lib.KDA_CONV_SILU if silu else 0, st)
+    if status:
+        _raise(status, "kda_conv_step")
     return y
 
 
@@ -293,22 +304,25 @@ def _conv_bwd(x, weight, bias, cu, N, T, s0, gy, gsT, silu, want_gs0, stream, wo
     gyp = _dense(gy, "grad_y", x.shape, _F32, dev)
     gsTp = _dense(gsT, "grad_final_state", (N, W - 1, D), _F32, dev)
     nbytes = conv_bwd_workspace_size(T if cu is not None else N * T, D, W)
-    with _on(dev, stream) as st:
-        gx, gw = x.new_empty(x.shape, dtype=_F32), torch.empty_like(weight)
-        gb = torch.empty_like(bias) if bias is not None else None
-        gs0 = x.new_empty((N, W - 1, D), dtype=_F32) if want_gs0 else None
-        ws, n, _keep = _scratch(nbytes, workspace, x)
-        grads = (gx.data_ptr(), gw.data_ptr(), _ptr(gb), _ptr(gs0))
-        mode = _lib.KDA_CONV_SILU if silu else 0
-        if cu is None:
-            status = _entry("kda_conv_bwd")(xp, ldx, wp, bp, s0p, gyp, gsTp, *grads, N, T, D, W, code, mode, ws, n, st)
-            if status:
-                _raise(status, "kda_conv_bwd")
-        else:
-            status = _entry("kda_conv_varlen_bwd")(
-                xp, ldx, wp, bp, cu.data_ptr(), N, s0p, gyp, gsTp, *grads, T, D, W, code, mode, ws, n, st)
-            if status:
-                _raise(status, "kda_conv_varlen_bwd")
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return _conv_bwd(x, weight, bias, cu, N, T, s0, gy, gsT, silu, want_gs0, None, workspace)
+    st = _raw_stream(dev)
+    gx, gw = x.new_empty(x.shape, dtype=_F32), torch.empty_like(weight)
+    gb = torch.empty_like(bias) if bias is not None else None
+    gs0 = x.new_empty((N, W - 1, D), dtype=_F32) if want_gs0 else None
+    ws, n, _keep = _scratch(nbytes, workspace, x)
+    grads = (gx.data_ptr(), gw.data_ptr(), _ptr(gb), _ptr(gs0))
+    mode = _lib.KDA_CONV_SILU if silu else 0
+    if cu is None:
+        status = _entry("kda_conv_bwd")(xp, ldx, wp, bp, s0p, gyp, gsTp, *grads, N, T, D, W, code, mode, ws, n, st)
+        if status:
+            _raise(status, "kda_conv_bwd")
+    else:
+        status = _entry("kda_conv_varlen_bwd")(
+            xp, ldx, wp, bp, cu.data_ptr(), N, s0p, gyp, gsTp, *grads, T, D, W, code, mode, ws, n, st)
+        if status:
+            _raise(status, "kda_conv_varlen_bwd")
     return gx, gw, gb, gs0
 
 
@@ -369,23 +383,26 @@ def _ssm_fwd(x, dt, A, B, C, cu, N, T, skip, z, dt_bias, s0, softplus, y, sT, wa
     s0p = _dense(s0, "initial_state", (N, D, S), _F32, dev)
     yp = _dense(y, "y", x.shape, o_dtype, dev)
     sTp = _dense(sT, "final_state", (N, D, S), _F32, dev)
-    with _on(dev, stream) as st:
-        if y is None:
-            y = _new(x, ins[1], o_dtype)
-            yp = y.data_ptr()
-        if sT is None and want_state:
-            sT = x.new_empty((N, D, S), dtype=_F32)
-            sTp = sT.data_ptr()
-        mode = _lib.KDA_SSM_SOFTPLUS if softplus else 0
-        if cu is None:
-            status = _entry("kda_ssm_fwd")(*ins, s0p, yp, sTp, N, T, D, S, G, code, o_code, mode, st)
-            if status:
-                _raise(status, "kda_ssm_fwd")
-        else:
-            status = _entry("kda_ssm_varlen_fwd")(
-                *ins, cu.data_ptr(), N, s0p, yp, sTp, T, D, S, G, code, o_code, mode, st)
-            if status:
-                _raise(status, "kda_ssm_varlen_fwd")
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return _ssm_fwd(x, dt, A, B, C, cu, N, T, skip, z, dt_bias, s0, softplus, y, sT, want_state, o_dtype, None)
+    st = _raw_stream(dev)
+    if y is None:
+        y = _new(x, ins[1], o_dtype)
+        yp = y.data_ptr()
+    if sT is None and want_state:
+        sT = torch.empty_like(s0) if s0 is not None else x.new_empty((N, D, S), dtype=_F32)
+        sTp = sT.data_ptr()
+    mode = _lib.KDA_SSM_SOFTPLUS if softplus else 0
+    if cu is None:
+        status = _entry("kda_ssm_fwd")(*ins, s0p, yp, sTp, N, T, D, S, G, code, o_code, mode, st)
+        if status:
+            _raise(status, "kda_ssm_fwd")
+    else:
+        status = _entry("kda_ssm_varlen_fwd")(
+            *ins, cu.data_ptr(), N, s0p, yp, sTp, T, D, S, G, code, o_code, mode, st)
+        if status:
+            _raise(status, "kda_ssm_varlen_fwd")
     return y, sT
 
 
@@ -399,14 +416,17 @@ def kda_ssm_step(x, dt, A, B, C, state, skip=None, z=None, dt_bias=None, *, soft
     ins, S, G = _ssm_in(x, dt, A, B, C, skip, z, dt_bias)
     sp = _dense(state, "state", (N, D, S), _F32, dev)
     yp = _dense(y, "y", x.shape, o_dtype, dev)
-    with _on(dev, stream) as st:
-        if y is None:
-            y = _new(x, ins[1], o_dtype)
-            yp = y.data_ptr()
-        status = _entry("kda_ssm_step")(
-            *ins, sp, yp, N, D, S, G, code, o_code, _lib.KDA_SSM_SOFTPLUS if softplus else 0, st)
-        if status:
-            _raise(status, "kda_ssm_step")
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return kda_ssm_step(x, dt, A, B, C, state, skip, z, dt_bias, softplus=softplus, y=y, o_dtype=o_dtype)
+    st = _raw_stream(dev)
+    if y is None:
+        y = _new(x, ins[1], o_dtype)
+        yp = y.data_ptr()
+    status = _entry("kda_ssm_step")(
+        *ins, sp, yp, N, D, S, G, code, o_code, _lib.KDA_SSM_SOFTPLUS if softplus else 0, st)
+    if status:
+        _raise(status, "kda_ssm_step")
     return y
 
 
@@ -440,25 +460,29 @@ def _ssm_bwd(x, dt, A, B, C, cu, N, T, skip, z, dt_bias, s0, gy, gsT, softplus, 
     gsTp = _dense(gsT, "grad_final_state", (N, D, S), _F32, dev)
     nbytes = _lib.workspace_size("kda_ssm_bwd_workspace_size" if cu is None else "kda_ssm_varlen_bwd_workspace_size",
                                  N, T, D, S, G, code)
-    with _on(dev, stream) as st:
-        f32 = dict(dtype=_F32)
-        gx, gdt, gA = x.new_empty(x.shape, **f32), x.new_empty(x.shape, **f32), torch.empty_like(A)
-        gB, gC = x.new_empty(B.shape, **f32), x.new_empty(C.shape, **f32)
-        gskip = torch.empty_like(skip) if skip is not None else None
-        gz = x.new_empty(x.shape, **f32) if z is not None else None
-        gbias = torch.empty_like(dt_bias) if dt_bias is not None else None
-        gs0 = x.new_empty((N, D, S), **f32) if want_gs0 else None
-        ws, n, _keep = _scratch(nbytes, workspace, x)
-        grads = (gx, gdt, gA, gB, gC, gskip, gz, gbias, gs0)
-        mode = _lib.KDA_SSM_SOFTPLUS if softplus else 0
-        if cu is None:
-            status = _entry("kda_ssm_bwd")(
-                *ins, s0p, gyp, gsTp, *map(_ptr, grads), N, T, D, S, G, code, mode, ws, n, st)
-            if status:
-                _raise(status, "kda_ssm_bwd")
-        else:
-            status = _entry("kda_ssm_varlen_bwd")(
-                *ins, cu.data_ptr(), N, s0p, gyp, gsTp, *map(_ptr, grads), T, D, S, G, code, mode, ws, n, st)
-            if status:
-                _raise(status, "kda_ssm_varlen_bwd")
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return _ssm_bwd(x, dt, A, B, C, cu, N, T, skip, z, dt_bias, s0, gy, gsT, softplus, want_gs0, None,
+                            workspace)
+    st = _raw_stream(dev)
+    f32 = dict(dtype=_F32)
+    gx, gdt, gA = x.new_empty(x.shape, **f32), x.new_empty(x.shape, **f32), torch.empty_like(A)
+    gB, gC = x.new_empty(B.shape, **f32), x.new_empty(C.shape, **f32)
+    gskip = torch.empty_like(skip) if skip is not None else None
+    gz = x.new_empty(x.shape, **f32) if z is not None else None
+    gbias = torch.empty_like(dt_bias) if dt_bias is not None else None
+    gs0 = x.new_empty((N, D, S), **f32) if want_gs0 else None
+    ws, n, _keep = _scratch(nbytes, workspace, x)
+    grads = (gx, gdt, gA, gB, gC, gskip, gz, gbias, gs0)
+    mode = _lib.KDA_SSM_SOFTPLUS if softplus else 0
+    if cu is None:
+        status = _entry("kda_ssm_bwd")(
+            *ins, s0p, gyp, gsTp, *map(_ptr, grads), N, T, D, S, G, code, mode, ws, n, st)
+        if status:
+            _raise(status, "kda_ssm_bwd")
+    else:
+        status = _entry("kda_ssm_varlen_bwd")(
+            *ins, cu.data_ptr(), N, s0p, gyp, gsTp, *map(_ptr, grads), T, D, S, G, code, mode, ws, n, st)
+        if status:
+            _raise(status, "kda_ssm_varlen_bwd")
     return grads
