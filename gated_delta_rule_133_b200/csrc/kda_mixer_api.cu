@@ -5,6 +5,7 @@
 namespace {
 
 constexpr int kMaxChannels = 1 << 20;
+constexpr long long kMaxTokens = 0x7fff0000LL;   // token indices and a tile beyond them stay below 2^31
 
 // Row stride of a token-major input: whole 16-byte vectors, rows that do not
 // overlap, below 4 GiB.
@@ -24,7 +25,7 @@ kda_status check_conv(const kda::ConvArgs& a, const void* y, const void* s0, con
         return KDA_ERR_INVALID_ARG;
     if (a.tokens > 0 && (!a.x || !y || !aligned16(a.x) || !aligned16(y) || !valid_ld(a.ldx, a.D, a.dtype)))
         return KDA_ERR_INVALID_ARG;
-    if (a.W < 2 || a.W > 4 || a.D % 8 != 0 || a.D > kMaxChannels || a.tokens > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if (a.W < 2 || a.W > 4 || a.D % 8 != 0 || a.D > kMaxChannels || a.tokens > kMaxTokens) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -107,7 +108,7 @@ kda_status check_ssm(const kda::SsmArgs& a, const void* y, int mode)
     }
     const kda_status st = check_ssm_sizes(a.D, a.N, a.G, a.dtype);
     if (st != KDA_OK) return st;
-    return a.tokens > 0x7fffffffLL ? KDA_ERR_UNSUPPORTED : KDA_OK;
+    return a.tokens > kMaxTokens ? KDA_ERR_UNSUPPORTED : KDA_OK;
 }
 
 kda_status ssm_fwd_call(const kda::SsmArgs& a, void* y, float* sT, kda_dtype o_dtype, int mode, void* stream)
@@ -210,7 +211,7 @@ kda_status kda_conv_varlen_bwd(const void* x, long long ldx, const float* weight
 kda_status kda_conv_bwd_workspace_size(long long tokens, int D, int W, size_t* bytes)
 {
     if (!bytes || tokens < 0 || D <= 0 || W <= 0) return KDA_ERR_INVALID_ARG;
-    if (W < 2 || W > 4 || D % 8 != 0 || D > kMaxChannels || tokens > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if (W < 2 || W > 4 || D % 8 != 0 || D > kMaxChannels || tokens > kMaxTokens) return KDA_ERR_UNSUPPORTED;
     *bytes = tokens == 0 ? 0 : kda::conv_bwd_workspace(tokens, D, W);
     return KDA_OK;
 }
@@ -276,7 +277,7 @@ kda_status kda_ssm_bwd_workspace_size(int B, int T, int D, int S, int G, kda_dty
     const kda_status st = check_ssm_sizes(D, S, G, dtype);
     if (st != KDA_OK) return st;
     const long long tokens = (long long)B * T;
-    if (tokens > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if (tokens > kMaxTokens) return KDA_ERR_UNSUPPORTED;
     *bytes = tokens == 0 ? 0 : kda::ssm_bwd_workspace(B, T, tokens, D, S, G, false);
     return KDA_OK;
 }
@@ -304,6 +305,7 @@ kda_status kda_ssm_varlen_bwd_workspace_size(int N, int T, int D, int S, int G, 
     if (!bytes || N < 0 || N > 65535 || T < 0) return KDA_ERR_INVALID_ARG;
     const kda_status st = check_ssm_sizes(D, S, G, dtype);
     if (st != KDA_OK) return st;
+    if (T > kMaxTokens) return KDA_ERR_UNSUPPORTED;
     *bytes = (N == 0 || T == 0) ? 0 : kda::ssm_bwd_workspace(N, T, T, D, S, G, true);
     return KDA_OK;
 }

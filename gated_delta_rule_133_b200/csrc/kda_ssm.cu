@@ -232,57 +232,59 @@ ssm_step_kernel(const SsmDev p, int n_seq)
     if (d >= p.D) return;   // D is a multiple of 8: whole groups of L <= 16 lanes leave together
     const unsigned mask = __activemask();
     const int lane = threadIdx.x & 31, group = lane / L * L;
-    const int bn = d / (p.D / p.G) * N + 4 * l, i0 = blockIdx.y * RN;
-    float4* state = reinterpret_cast<float4*>(p.sT) + ((long long)i0 * p.D + d) * L + l;
-    const long long next = (long long)p.D * L;      // 16-byte vectors from sequence to sequence
-    const int rows = min(RN, n_seq - i0);
-    float4 h[RN];
-#pragma unroll
-    for (int r = 0; r < RN; ++r) {
-        if (r < rows) {
-            h[r] = __ldcs(state + r * next);
-        }
-    }
-    const int mine = RN == 1 ? 0 : l / (L / 4);     // the sequence whose elements are this lane's
-    float x = 0.f, delta = 0.f, z = 0.f;
-    if (mine < rows) {
-        x = Elem<T>::load(row<T>(p.x, i0 + mine, p.ldx) + d);
-        delta = Elem<T>::load(row<T>(p.dt, i0 + mine, p.lddt) + d);
-        if (p.z) z = Elem<T>::load(row<T>(p.z, i0 + mine, p.ldz) + d);
-    }
+    const int bn = d / (p.D / p.G) * N + 4 * l;
     float4 A = *reinterpret_cast<const float4*>(p.A + (long long)d * N + 4 * l);
     A.x *= kLog2e; A.y *= kLog2e; A.z *= kLog2e; A.w *= kLog2e;
-    if (p.dt_bias) delta += p.dt_bias[d];
-    if (p.softplus) delta = softplus(delta);
-    const float u = delta * x;
-    float y[RN];
+    for (int i0 = blockIdx.y * RN; i0 < n_seq; i0 += gridDim.y * RN) {   // one round unless n_seq is beyond the grid
+        float4* state = reinterpret_cast<float4*>(p.sT) + ((long long)i0 * p.D + d) * L + l;
+        const long long next = (long long)p.D * L;      // 16-byte vectors from sequence to sequence
+        const int rows = min(RN, n_seq - i0);
+        float4 h[RN];
 #pragma unroll
-    for (int r = 0; r < RN; ++r) {
-        const float dr = RN == 1 ? delta : __shfl_sync(mask, delta, group + r * (L / 4));
-        const float ur = RN == 1 ? u : __shfl_sync(mask, u, group + r * (L / 4));
-        y[r] = 0.f;
-        if (r < rows) {
-            float b[4], c[4];   // read here: held from the start they would halve the blocks per SM
-            load_vec<4>(row<T>(p.b, i0 + r, p.ldb) + bn, b);
-            load_vec<4>(row<T>(p.c, i0 + r, p.ldc) + bn, c);
-            h[r].x = fmaf(exp2_approx(fmaf(dr, A.x, kDecayShift)), h[r].x, ur * b[0]);
-            h[r].y = fmaf(exp2_approx(fmaf(dr, A.y, kDecayShift)), h[r].y, ur * b[1]);
-            h[r].z = fmaf(exp2_approx(fmaf(dr, A.z, kDecayShift)), h[r].z, ur * b[2]);
-            h[r].w = fmaf(exp2_approx(fmaf(dr, A.w, kDecayShift)), h[r].w, ur * b[3]);
-            __stcs(state + r * next, h[r]);
-            y[r] = fmaf(c[0], h[r].x, c[1] * h[r].y) + fmaf(c[2], h[r].z, c[3] * h[r].w);
+        for (int r = 0; r < RN; ++r) {
+            if (r < rows) {
+                h[r] = __ldcs(state + r * next);
+            }
         }
-    }
-    reduce_transposed<RN, RN, L / RN>(y, lane, mask);
+        const int mine = RN == 1 ? 0 : l / (L / 4);     // the sequence whose elements are this lane's
+        float x = 0.f, delta = 0.f, z = 0.f;
+        if (mine < rows) {
+            x = Elem<T>::load(row<T>(p.x, i0 + mine, p.ldx) + d);
+            delta = Elem<T>::load(row<T>(p.dt, i0 + mine, p.lddt) + d);
+            if (p.z) z = Elem<T>::load(row<T>(p.z, i0 + mine, p.ldz) + d);
+        }
+        if (p.dt_bias) delta += p.dt_bias[d];
+        if (p.softplus) delta = softplus(delta);
+        const float u = delta * x;
+        float y[RN];
 #pragma unroll
-    for (int m = L / RN / 2; m >= 1; m >>= 1) y[0] += __shfl_xor_sync(mask, y[0], m);
-    if (l % (L / RN) == 0 && mine < rows) {
-        float out = p.skip ? fmaf(p.skip[d], x, y[0]) : y[0];
-        if (p.z) out *= silu(z);
-        if (p.o_bf16)
-            row<__nv_bfloat16>(p.y, i0 + mine, 2u * p.D)[d] = __float2bfloat16_rn(out);
-        else
-            row<float>(p.y, i0 + mine, 4u * p.D)[d] = out;
+        for (int r = 0; r < RN; ++r) {
+            const float dr = RN == 1 ? delta : __shfl_sync(mask, delta, group + r * (L / 4));
+            const float ur = RN == 1 ? u : __shfl_sync(mask, u, group + r * (L / 4));
+            y[r] = 0.f;
+            if (r < rows) {
+                float b[4], c[4];   // read here: held from the start they would halve the blocks per SM
+                load_vec<4>(row<T>(p.b, i0 + r, p.ldb) + bn, b);
+                load_vec<4>(row<T>(p.c, i0 + r, p.ldc) + bn, c);
+                h[r].x = fmaf(exp2_approx(fmaf(dr, A.x, kDecayShift)), h[r].x, ur * b[0]);
+                h[r].y = fmaf(exp2_approx(fmaf(dr, A.y, kDecayShift)), h[r].y, ur * b[1]);
+                h[r].z = fmaf(exp2_approx(fmaf(dr, A.z, kDecayShift)), h[r].z, ur * b[2]);
+                h[r].w = fmaf(exp2_approx(fmaf(dr, A.w, kDecayShift)), h[r].w, ur * b[3]);
+                __stcs(state + r * next, h[r]);
+                y[r] = fmaf(c[0], h[r].x, c[1] * h[r].y) + fmaf(c[2], h[r].z, c[3] * h[r].w);
+            }
+        }
+        reduce_transposed<RN, RN, L / RN>(y, lane, mask);
+#pragma unroll
+        for (int m = L / RN / 2; m >= 1; m >>= 1) y[0] += __shfl_xor_sync(mask, y[0], m);
+        if (l % (L / RN) == 0 && mine < rows) {
+            float out = p.skip ? fmaf(p.skip[d], x, y[0]) : y[0];
+            if (p.z) out *= silu(z);
+            if (p.o_bf16)
+                row<__nv_bfloat16>(p.y, i0 + mine, 2u * p.D)[d] = __float2bfloat16_rn(out);
+            else
+                row<float>(p.y, i0 + mine, 4u * p.D)[d] = out;
+        }
     }
 }
 
@@ -324,11 +326,11 @@ template <typename T, int N>
 static cudaError_t launch_step(const SsmArgs& a, const SsmDev& p, cudaStream_t s)
 {
     const unsigned gx = (unsigned)(((long long)a.D * (N / 4) + 255) / 256);
-    // four sequences per thread once that leaves 2048 threads per SM (or the grid's
-    // second dimension would run out)
+    // four sequences per thread once that leaves 2048 threads per SM, or where the
+    // grid's second dimension would run out
     if ((long long)gx * a.nseq / 4 >= 148LL * 8 || a.nseq > 65535) {
-        if ((a.nseq + 3) / 4 > 65535) return cudaErrorInvalidConfiguration;
-        ssm_step_kernel<T, N, 4><<<dim3(gx, (a.nseq + 3) / 4), 256, 0, s>>>(p, a.nseq);
+        const int blocks = (int)(((long long)a.nseq + 3) / 4);
+        ssm_step_kernel<T, N, 4><<<dim3(gx, blocks < 65535 ? blocks : 65535), 256, 0, s>>>(p, a.nseq);
     } else {
         ssm_step_kernel<T, N, 1><<<dim3(gx, a.nseq), 256, 0, s>>>(p, a.nseq);
     }

@@ -6,6 +6,14 @@
 namespace kda {
 namespace mixer {
 
+// max(a, b), NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // softplus(v) = max(v, 0) + log(1 + e), e = e^-|v|, of two values, to fp32 accuracy
 // for every v.  e: 2^(-|v| log2 e) with the rounding error of the exponent put back
 // (log2 e in two parts).  log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, without
@@ -14,7 +22,9 @@ namespace mixer {
 __device__ __forceinline__ f32x2 softplus2(float v0, float v1)
 {
     auto two = [](float x) { return pack(x, x); };
-    const f32x2 t = pack(-fabsf(v0), -fabsf(v1));
+    // below e^-100 the result is zero; without the bound the rounding error of an
+    // infinite exponent (a token masked by the lowest value or -inf) would be NaN
+    const f32x2 t = pack(max_nan(-fabsf(v0), -100.f), max_nan(-fabsf(v1), -100.f));
     const f32x2 nhi = mul2(t, two(-kLog2e));
     const f32x2 lo = fma2(t, two(1.9259629e-8f), fma2(t, two(kLog2e), nhi));
     float h0, h1;

@@ -292,6 +292,48 @@ def test_ssm_non_finite_inputs_stay_in_their_channel_and_future():
     assert not torch.isfinite(sT[0, 3]).any() and torch.isfinite(sT[0, [0, 1, 2, 4, 6]]).all()
 
 
+@pytest.mark.parametrize("mask", [float("-inf"), torch.finfo(torch.bfloat16).min, -1e4])
+def test_ssm_masked_tokens_leave_the_state(mask):
+    """A step size of softplus(-inf), of the type's lowest value or of a large negative
+    number is zero: the state passes the token unchanged (prompt and step), the token's
+    gradients of x and dt are those of the skip and zero."""
+    T, D, S = 30, 16, 16
+    p, cu, gy, gsT = _inputs([T], D, S, 1, torch.bfloat16, 43, bias=False)
+    masked = [0, 7, 8, 21, T - 1]
+    p["dt"][masked] = mask
+    q = dict(p, dt=p["dt"].clone())
+    q["dt"][masked] = -1e4                       # for the oracle: softplus(-1e4) = 0 in 64 bits
+    d = _lead(_dev(p), 1, T)
+    y, sT = _fwd(d, o_dtype=torch.float32)
+    _check_fwd(q, cu, (y[0], sT), {})
+    grads = _bwd(d, gy.to(DEV).view(1, T, D), gsT.to(DEV))
+    _check_bwd(q, cu, grads, gy, gsT)
+    assert (grads[1][0, masked] == 0).all()
+    state = d["s0"].clone()
+    out = kda.kda_ssm_step(d["x"][:, 7], d["dt"][:, 7], d["A"], d["B"][:, 7], d["C"][:, 7], state, d["skip"], d["z"][:, 7])
+    assert torch.equal(state, d["s0"]) and torch.isfinite(out.float()).all()
+
+
+def test_ssm_nan_step_size_is_not_hidden():
+    p, cu, _, _ = _inputs([12], 16, 16, 1, torch.float32, 44)
+    p["dt"][5, 2] = float("nan")
+    y, sT = _fwd(_lead(_dev(p), 1, 12))
+    bad = ~torch.isfinite(y[0])
+    assert bad[5:, 2].all() and bad.sum() == 7 and torch.isnan(sT[0, 2]).all()
+
+
+def test_ssm_step_beyond_the_grid():
+    """More sequences than one grid holds: every one is advanced."""
+    N, D, S = 70000 * 4, 8, 16
+    x = torch.ones(N, D, device=DEV)
+    state = torch.arange(N, device=DEV, dtype=torch.float32).view(N, 1, 1).expand(N, D, S).contiguous()
+    zero = torch.zeros(D, S, device=DEV)
+    y = kda.kda_ssm_step(x, x, zero, torch.ones(N, 1, S, device=DEV), torch.ones(N, 1, S, device=DEV), state, softplus=False)
+    want = torch.arange(N, device=DEV, dtype=torch.float32) + 1      # exact: decay 2^0, input 1, below 2^24
+    assert torch.equal(state, want.view(N, 1, 1).expand(N, D, S))
+    assert torch.equal(y, (want * S).view(N, 1).expand(N, D))
+
+
 def test_ssm_streams_graphs_and_dirty_workspace():
     """A side stream, a captured graph and a workspace full of garbage give the
     eager result, bit for bit, forward and backward."""
