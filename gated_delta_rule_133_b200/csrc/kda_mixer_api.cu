@@ -17,6 +17,18 @@ bool valid_ld(long long ld, long long row, kda_dtype dtype)
 
 bool opt_aligned16(const void* p) { return !p || aligned16(p); }
 
+// Whether rows of `row` elements, `ld` apart, and the dense output y [tokens, D]
+// share memory: an output written while other blocks still read the input.
+bool overlaps(const void* in, long long ld, long long row, kda_dtype dtype, const void* y, long long D,
+              kda_dtype o_dtype, long long tokens)
+{
+    if (!in || tokens == 0) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(y);
+    const uintptr_t na = (uintptr_t)((tokens - 1) * ld + row) * (dtype == KDA_BF16 ? 2 : 4);
+    const uintptr_t nb = (uintptr_t)(tokens * D) * (o_dtype == KDA_BF16 ? 2 : 4);
+    return a < b + nb && b < a + na;
+}
+
 kda_status check_conv(const kda::ConvArgs& a, const void* y, const void* s0, const void* sT, int mode)
 {
     if (a.tokens < 0 || a.nseq < 0 || a.D <= 0 || a.W <= 0 || !valid_dtype(a.dtype) || (mode & ~KDA_CONV_SILU))
@@ -56,7 +68,8 @@ kda_status conv_fwd_call(const kda::ConvArgs& a, const void* s0, void* y, void* 
 {
     const kda_status st = check_conv(a, y, s0, sT, mode);
     if (st != KDA_OK) return st;
-    if (!valid_dtype(o_dtype)) return KDA_ERR_INVALID_ARG;
+    if (!valid_dtype(o_dtype) || overlaps(a.x, a.ldx, a.D, a.dtype, y, a.D, o_dtype, a.tokens))
+        return KDA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t es = a.dtype == KDA_BF16 ? 2 : 4;
     if (a.tokens == 0) return copy_bytes(s0, sT, (size_t)a.nseq * (a.W - 1) * a.D * es, s);
@@ -111,11 +124,21 @@ kda_status check_ssm(const kda::SsmArgs& a, const void* y, int mode)
     return a.tokens > kMaxTokens ? KDA_ERR_UNSUPPORTED : KDA_OK;
 }
 
+bool ssm_overlap(const kda::SsmArgs& a, const void* y, kda_dtype o_dtype)
+{
+    const long long gs = (long long)a.G * a.N;
+    auto hit = [&](const void* in, long long ld, long long row) {
+        return overlaps(in, ld, row, a.dtype, y, a.D, o_dtype, a.tokens);
+    };
+    return hit(a.x, a.ldx, a.D) || hit(a.dt, a.lddt, a.D) || hit(a.b, a.ldb, gs) || hit(a.c, a.ldc, gs) ||
+           hit(a.z, a.ldz, a.D);
+}
+
 kda_status ssm_fwd_call(const kda::SsmArgs& a, void* y, float* sT, kda_dtype o_dtype, int mode, void* stream)
 {
     const kda_status st = check_ssm(a, y, mode);
     if (st != KDA_OK) return st;
-    if (!valid_dtype(o_dtype) || !opt_aligned16(sT)) return KDA_ERR_INVALID_ARG;
+    if (!valid_dtype(o_dtype) || !opt_aligned16(sT) || ssm_overlap(a, y, o_dtype)) return KDA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.tokens == 0) return copy_state(a.s0, sT, (size_t)a.nseq * a.D * a.N, s);
     return from_cuda(kda::ssm_fwd(a, y, sT, o_dtype, s));
@@ -179,7 +202,8 @@ kda_status kda_conv_step(const void* x, long long ldx, const float* weight, cons
     const kda::ConvArgs a = conv_args(x, ldx, weight, bias, nullptr, N, 1, N, D, W, dtype, mode);
     const kda_status st = check_conv(a, y, state, nullptr, mode);
     if (st != KDA_OK) return st;
-    if (!valid_dtype(o_dtype) || (N > 0 && !state)) return KDA_ERR_INVALID_ARG;
+    if (!valid_dtype(o_dtype) || (N > 0 && !state) || overlaps(x, ldx, D, dtype, y, D, o_dtype, N))
+        return KDA_ERR_INVALID_ARG;
     if (N == 0) return KDA_OK;
     return from_cuda(kda::conv_step(a, state, y, o_dtype, static_cast<cudaStream_t>(stream)));
 }
@@ -250,7 +274,8 @@ kda_status kda_ssm_step(const void* x, long long ldx, const void* dt, long long 
                          N, D, S, G, (mode & KDA_SSM_SOFTPLUS) != 0, dtype};
     const kda_status st = check_ssm(a, y, mode);
     if (st != KDA_OK) return st;
-    if (!valid_dtype(o_dtype) || (N > 0 && (!state || !aligned16(state)))) return KDA_ERR_INVALID_ARG;
+    if (!valid_dtype(o_dtype) || (N > 0 && (!state || !aligned16(state))) || ssm_overlap(a, y, o_dtype))
+        return KDA_ERR_INVALID_ARG;
     if (N == 0) return KDA_OK;
     return from_cuda(kda::ssm_step(a, state, y, o_dtype, static_cast<cudaStream_t>(stream)));
 }

@@ -76,7 +76,7 @@ ssm_walk_kernel(const SsmDev p, const WalkBwd wb)
 #pragma unroll
     for (int n = 0; n < NPT / 2; ++n) {
         const float2 a = *reinterpret_cast<const float2*>(p.A + (long long)(c0 + c) * N + l * NPT + 2 * n);
-        A2[n] = pack(a.x * kLog2e, a.y * kLog2e);
+        A2[n] = pack(bounded_decay(a.x) * kLog2e, bounded_decay(a.y) * kLog2e);
         h[n] = p.s0 ? *reinterpret_cast<const f32x2*>(p.s0 + srow + 2 * n) : 0ull;
     }
     const bool gated = p.z != nullptr;
@@ -229,12 +229,14 @@ ssm_step_kernel(const SsmDev p, int n_seq)
     constexpr int L = N / 4;
     const int f = blockIdx.x * 256 + threadIdx.x;   // 16-byte vector within one sequence's state (D N / 4 < 2^24)
     const int d = f / L, l = f % L;
-    if (d >= p.D) return;   // D is a multiple of 8: whole groups of L <= 16 lanes leave together
-    const unsigned mask = __activemask();
+    if (d >= p.D) return;   // D is a multiple of 8 and 32 / L divides 8: whole warps leave
     const int lane = threadIdx.x & 31, group = lane / L * L;
     const int bn = d / (p.D / p.G) * N + 4 * l;
     float4 A = *reinterpret_cast<const float4*>(p.A + (long long)d * N + 4 * l);
-    A.x *= kLog2e; A.y *= kLog2e; A.z *= kLog2e; A.w *= kLog2e;
+    A.x = bounded_decay(A.x) * kLog2e;
+    A.y = bounded_decay(A.y) * kLog2e;
+    A.z = bounded_decay(A.z) * kLog2e;
+    A.w = bounded_decay(A.w) * kLog2e;
     for (int i0 = blockIdx.y * RN; i0 < n_seq; i0 += gridDim.y * RN) {   // one round unless n_seq is beyond the grid
         float4* state = reinterpret_cast<float4*>(p.sT) + ((long long)i0 * p.D + d) * L + l;
         const long long next = (long long)p.D * L;      // 16-byte vectors from sequence to sequence
@@ -242,9 +244,7 @@ ssm_step_kernel(const SsmDev p, int n_seq)
         float4 h[RN];
 #pragma unroll
         for (int r = 0; r < RN; ++r) {
-            if (r < rows) {
-                h[r] = __ldcs(state + r * next);
-            }
+            if (r < rows) h[r] = __ldcs(state + r * next);
         }
         const int mine = RN == 1 ? 0 : l / (L / 4);     // the sequence whose elements are this lane's
         float x = 0.f, delta = 0.f, z = 0.f;
@@ -259,8 +259,8 @@ ssm_step_kernel(const SsmDev p, int n_seq)
         float y[RN];
 #pragma unroll
         for (int r = 0; r < RN; ++r) {
-            const float dr = RN == 1 ? delta : __shfl_sync(mask, delta, group + r * (L / 4));
-            const float ur = RN == 1 ? u : __shfl_sync(mask, u, group + r * (L / 4));
+            const float dr = RN == 1 ? delta : __shfl_sync(0xffffffffu, delta, group + r * (L / 4));
+            const float ur = RN == 1 ? u : __shfl_sync(0xffffffffu, u, group + r * (L / 4));
             y[r] = 0.f;
             if (r < rows) {
                 float b[4], c[4];   // read here: held from the start they would halve the blocks per SM
@@ -274,9 +274,9 @@ ssm_step_kernel(const SsmDev p, int n_seq)
                 y[r] = fmaf(c[0], h[r].x, c[1] * h[r].y) + fmaf(c[2], h[r].z, c[3] * h[r].w);
             }
         }
-        reduce_transposed<RN, RN, L / RN>(y, lane, mask);
+        reduce_transposed<RN, RN, L / RN>(y, lane);
 #pragma unroll
-        for (int m = L / RN / 2; m >= 1; m >>= 1) y[0] += __shfl_xor_sync(mask, y[0], m);
+        for (int m = L / RN / 2; m >= 1; m >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], m);
         if (l % (L / RN) == 0 && mine < rows) {
             float out = p.skip ? fmaf(p.skip[d], x, y[0]) : y[0];
             if (p.z) out *= silu(z);

@@ -46,6 +46,12 @@ __device__ __forceinline__ float softplus(float v)
     return r;
 }
 
+// A, kept from infinity: a rate of -inf would make 0 * inf of a step size of zero (a
+// masked token, or one that fills up a turn behind the last token), and a sum of
+// w A beyond the largest number inf * 0 of its gradient.  Below -1e30 every step
+// size above 1e-28 forgets everything.
+__device__ __forceinline__ float bounded_decay(float a) { return max_nan(a, -1e30f); }
+
 // Decays 2^(Delta A2) of two states.  ex2.approx is below the true value by 0.4
 // 2^-24 on average for exponents in [-0.25, -0.003] (measured), which hundreds of
 // slow decays in a row would add up; the exponent is moved by that much, at no
@@ -63,7 +69,7 @@ __device__ __forceinline__ f32x2 decay2(f32x2 delta, f32x2 A2)
 // i V / LANES and on, in p[0 .. V / LANES).  V - V / LANES shuffles instead of
 // V log2(LANES).
 template <int V, int LANES, int STRIDE, int P>
-__device__ __forceinline__ void reduce_transposed(float (&p)[P], int lane, unsigned mask = 0xffffffffu)
+__device__ __forceinline__ void reduce_transposed(float (&p)[P], int lane)
 {
     static_assert(V <= P && V % LANES == 0, "values");
     if constexpr (LANES > 1) {
@@ -72,9 +78,9 @@ __device__ __forceinline__ void reduce_transposed(float (&p)[P], int lane, unsig
         for (int j = 0; j < V / 2; ++j) {
             const float keep = up ? p[j + V / 2] : p[j];
             const float send = up ? p[j] : p[j + V / 2];
-            p[j] = keep + __shfl_xor_sync(mask, send, STRIDE * LANES / 2);
+            p[j] = keep + __shfl_xor_sync(0xffffffffu, send, STRIDE * LANES / 2);
         }
-        reduce_transposed<V / 2, LANES / 2, STRIDE>(p, lane, mask);
+        reduce_transposed<V / 2, LANES / 2, STRIDE>(p, lane);
     }
 }
 

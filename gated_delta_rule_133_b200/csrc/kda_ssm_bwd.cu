@@ -179,7 +179,7 @@ ssm_reverse_kernel(const BwdDev b)
     for (int i = threadIdx.x; i < SETS * 32 * NPT; i += K::THREADS) {
         // [set][lane][place]
         const int ch = i / N, of = i / NPT % 32, n = i % N ^ Order<N>::x_of(Order<N>::copy(of));
-        sA[i] = ch < sets * DT ? p.A[(long long)(c00 + ch) * N + n] : 0.f;
+        sA[i] = ch < sets * DT ? bounded_decay(p.A[(long long)(c00 + ch) * N + n]) : 0.f;
     }
     for (int i = threadIdx.x; i < W * SETS * 32 * NPT; i += K::THREADS) sGA[i] = 0.f;
     for (int i = threadIdx.x; i < W * SETS * K::EL * 4; i += K::THREADS) sGP[i] = 0.f;

@@ -375,7 +375,8 @@ kda_status kda_dplr_varlen_fwd_workspace_size(int N, int T, int H, int dk, int d
  *   weight   [D, W] fp32; bias [D] fp32 or NULL; 16-byte aligned
  *   initial_state / final_state [N, W - 1, D] of type `dtype` or NULL (final may
  *            be the same memory as initial); copies of inputs, never rounded
- *   y        [B, T, D] (dense) or [T, D] (packed), o_dtype, written
+ *   y        [B, T, D] (dense) or [T, D] (packed), o_dtype, written; must not
+ *            share memory with x (KDA_ERR_INVALID_ARG)
  *   mode     0 or KDA_CONV_SILU
  * D a multiple of 8, at most 2^20, W in {2, 3, 4}: others return
  * KDA_ERR_UNSUPPORTED.  Packed batches follow kda_varlen_fwd's rules: a sequence
@@ -434,15 +435,19 @@ kda_status kda_conv_bwd_workspace_size(long long tokens, int D, int W, size_t* b
  *
  * without the skip term, the gate or the bias where skip, z or dt_bias is NULL.
  * (With one decay per head instead, the recurrence is this library's layer with
- * KDA_MODE_HEAD_GATE | KDA_MODE_NO_ERASE.)  fp32 arithmetic and state.
+ * KDA_MODE_HEAD_GATE | KDA_MODE_NO_ERASE.)  fp32 arithmetic and state.  With
+ * KDA_SSM_SOFTPLUS a dt of -inf or of the type's lowest value is a step size of
+ * zero: a padded token with finite x, B, C leaves the state as it is, bit for bit.
  *
  *   x, dt, z   rows of D elements, B, C rows of G * S elements, all of type
  *              `dtype`; row (b, t) at pointer + (b T + t) * its ld, ld in elements,
  *              a multiple of 16 bytes, at least the row's length, below 2^30
- *   A          [D, S] fp32, <= 0 (not checked); skip, dt_bias [D] fp32 or NULL
+ *   A          [D, S] fp32, <= 0 (not checked; values below -1e30, -inf among
+ *              them, count as -1e30, so that a step size of zero keeps the state); skip, dt_bias [D] fp32 or NULL
  *   initial_state / final_state [N, D, S] fp32 or NULL (final may be the same
  *              memory as initial)
- *   y          [B, T, D] (dense) or [T, D] (packed), o_dtype, written
+ *   y          [B, T, D] (dense) or [T, D] (packed), o_dtype, written; must not
+ *              share memory with x, dt, B, C or z (KDA_ERR_INVALID_ARG)
  *   mode       0 or KDA_SSM_SOFTPLUS
  * D a multiple of 8 * G, at most 2^20, S in {16, 32, 64}: others return
  * KDA_ERR_UNSUPPORTED.  Pointers 16-byte aligned.  Packed batches follow

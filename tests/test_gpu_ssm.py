@@ -314,6 +314,27 @@ def test_ssm_masked_tokens_leave_the_state(mask):
     assert torch.equal(state, d["s0"]) and torch.isfinite(out.float()).all()
 
 
+@pytest.mark.parametrize("T", [1, 7, 8, 30])
+def test_ssm_infinite_decay_rate(T):
+    """A state with A = -inf forgets everything at a token whose step size is above zero
+    and keeps all of it at a masked one, whatever the length's remainder is."""
+    D, S = 16, 16
+    p, cu, gy, gsT = _inputs([T], D, S, 1, torch.bfloat16, 45, bias=False)
+    p["A"][1, 3] = p["A"][5] = float("-inf")
+    p["A"][7, 2] = torch.finfo(torch.float32).min
+    q = dict(p, A=p["A"].clone().clamp(min=-1e8), dt=p["dt"].clone())   # exp(-1e8 Delta) = 0 in 64 bits, Delta > 1e-5
+    for t in ([0] if T == 1 else [0, 3, T - 1]):
+        p["dt"][t] = float("-inf")
+        q["dt"][t] = -1e4
+    d = _lead(_dev(p), 1, T)
+    y, sT = _fwd(d, o_dtype=torch.float32)
+    _check_fwd(q, cu, (y[0], sT), {})
+    _check_bwd(q, cu, _bwd(d, gy.to(DEV).view(1, T, D), gsT.to(DEV)), gy, gsT)
+    state = d["s0"].clone()
+    kda.kda_ssm_step(d["x"][:, 0], d["dt"][:, 0], d["A"], d["B"][:, 0], d["C"][:, 0], state, d["skip"], d["z"][:, 0])
+    assert torch.equal(state, d["s0"])
+
+
 def test_ssm_nan_step_size_is_not_hidden():
     p, cu, _, _ = _inputs([12], 16, 16, 1, torch.float32, 44)
     p["dt"][5, 2] = float("nan")

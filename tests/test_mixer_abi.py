@@ -120,6 +120,23 @@ def test_ssm_varlen_step_and_bwd_validation():
     assert lib.kda_ssm_varlen_bwd_workspace_size(70000, 8, 64, 16, 1, BF16, ctypes.byref(out)) == BAD
 
 
+def test_outputs_that_share_memory_with_inputs():
+    """y written over an input that other blocks still read: refused by its range, the
+    rows' stride counted (bf16 inputs of 18 rows of 64, fp32 output: 2304 and 4608 bytes)."""
+    lib = _lib.load()
+    far = 1 << 24
+    for at in (dict(_0=far, _5=far), dict(_0=far, _5=far + 2288), dict(_0=far, _5=far - 4592),
+               dict(_0=far, _1=128, _5=far + 17 * 256 + 112)):
+        assert lib.kda_conv_fwd(*_with(CONV, **at)) == BAD, at
+    step = (far, 64, P, P, 8 * far, far + 256, 3, 64, 4, BF16, F32, 1, None)
+    assert lib.kda_conv_step(*step) == BAD
+    apart = [far * (i + 1) if v == P else v for i, v in enumerate(SSM)]
+    for i, rows in ((0, 64), (2, 64), (5, 32), (7, 32), (10, 64)):     # x, dt, B, C, z
+        assert lib.kda_ssm_fwd(*_with(apart, _14=apart[i] + 17 * 2 * rows)) == BAD, i
+    one = apart[:13] + [20 * far, apart[0], 3, 64, 16, 2, BF16, F32, 1, None]
+    assert lib.kda_ssm_step(*one) == BAD
+
+
 def test_python_refuses_what_does_not_fit():
     x, w = torch.zeros(2, 8, 16), torch.zeros(16, 4)
     for call, word in (
