@@ -8,9 +8,12 @@
 // element written once (plus a halo of W - 1 rows per token tile, which the L2
 // holds).  A thread owns four channels and walks a tile of tokens with the last
 // W - 1 rows and the weights in registers, so no shared memory or synchronisation
-// is needed and the loads of the next tokens are in flight together.  (Eight
-// channels per thread halve the requests but need twice the registers: 198, and
-// half the warps.)
+// is needed and the loads of the next tokens are in flight together.
+//
+// Measured (bf16 in and out, W = 4, SiLU, cold L2): 65536 x 2048 in 109 us, 4.9 TB/s
+// of 6.55 of a copy; 4096 x 2048 in 10.1 us.  Eight channels per thread halve the
+// requests but need 198 registers and half the warps: 320 us where four take 209.
+// Blocks of one token tile in a row instead of one channel block: the same.
 #include "kda_mixer.cuh"
 
 namespace kda {
@@ -109,9 +112,11 @@ __device__ __forceinline__ void put(TO* y, const f32x2 (&p)[2])
 }
 
 // Grid: x = token tiles of R tokens, then (if sT) one block per sequence for
-// the final states; y = channel blocks.  U tokens are loaded ahead.
+// the final states; y = channel blocks.  U tokens are loaded while the U before
+// them are summed (16384 x 2048: 31.4 us; loaded and summed in turn, six blocks per
+// SM instead of five: 32.7; U = 4: 30.7, but 11.5 instead of 10.1 at 4096 x 2048).
 template <typename T, typename TO, int W, bool SILU>
-__global__ void __launch_bounds__(128, 6)
+__global__ void __launch_bounds__(128, 5)
 conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ bias,
                 const T* s0, TO* __restrict__ y, T* sT, Seqs q, int D, int R, int ntiles)
 {
@@ -166,13 +171,23 @@ conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
             py += D;
         };
         int n = (int)(stop - t);
+        if (n >= U) {
+            Quad next[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u, px += ldx) next[u] = *reinterpret_cast<const Quad*>(px);
 #pragma unroll 1
-        for (; n >= U; n -= U) {
-            Quad raw[U];
+            for (; n >= 2 * U; n -= U) {
+                Quad raw[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u, px += ldx) raw[u] = *reinterpret_cast<const Quad*>(px);
+                for (int u = 0; u < U; ++u) raw[u] = next[u];
 #pragma unroll
-            for (int u = 0; u < U; ++u) step(raw[u]);
+                for (int u = 0; u < U; ++u, px += ldx) next[u] = *reinterpret_cast<const Quad*>(px);
+#pragma unroll
+                for (int u = 0; u < U; ++u) step(raw[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) step(next[u]);
+            n -= U;
         }
 #pragma unroll 1
         for (; n > 0; --n, px += ldx) step(*reinterpret_cast<const Quad*>(px));
@@ -182,7 +197,9 @@ conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
 
 // One token per sequence: y from the state's rows and x; the state moves up by
 // one row.  A thread owns a channel vector of RN sequences, so that the weights
-// are read once for them and all their rows are in flight together.
+// are read once for them and all their rows are in flight together.  1024 x 4096 in
+// bf16: 11.5 us for 75.5 MB, 6.6 TB/s, some of it from the L2; 16 sequences: 1.9 us,
+// a launch.
 template <typename T, typename TO, int W, bool SILU, int RN>
 __global__ void __launch_bounds__(128)
 conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ bias,
@@ -230,6 +247,12 @@ conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict
 // its own gx but does not add to gw and gb).  gw and gb of a tile go to a
 // partial sum of its own, part[tile][j][D] (j = W: the bias), which a second
 // kernel adds in a fixed order: no atomics, the same result every time.
+//
+// Ten bytes per element (x in bf16, gy, gx in fp32), so HBM is the bound; what it
+// reaches is set by the loads in flight, four blocks of 128 registers per SM.
+// 8192 x 2048: 44 + 4 us, 3.8 TB/s.  Two channels per thread 47 us and more; tiles
+// staged in shared memory by cp.async, two channels per thread, 45.5; U = 2, 6, 8 and
+// five to eight blocks per SM slower; channel blocks first in the grid 69.
 template <typename T, int W, bool SILU>
 __global__ void __launch_bounds__(128)
 conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ bias,
@@ -387,7 +410,8 @@ conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
 }
 
 // gw[d, j] and gb[d] from the tiles' partial sums: 32 columns per block, 32 rows
-// of threads over the tiles, then a sum over those rows.
+// of threads over the tiles, then a sum over those rows.  4 us for 128 tiles of
+// 2048 channels (5.2 MB, from the L2).
 __global__ void __launch_bounds__(1024)
 conv_bwd_reduce_kernel(const float* __restrict__ part, int ntiles, float* __restrict__ gw, float* __restrict__ gb,
                        int D, int W)
@@ -415,7 +439,8 @@ conv_bwd_reduce_kernel(const float* __restrict__ part, int ntiles, float* __rest
 
 // Gradient of the initial states: row k of sequence i is the input at position
 // k - (W - 1) before its first token, read by tokens m <= k; with len <= k
-// tokens it is also row k - len of the final state.
+// tokens it is also row k - len of the final state.  W - 1 rows of 2 W - 2 inputs per
+// sequence: a launch's time (5 us for two sequences of 2048 channels).
 template <typename T, int W, bool SILU>
 __global__ void __launch_bounds__(128)
 conv_bwd_state_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w,
@@ -471,12 +496,15 @@ conv_bwd_state_kernel(const T* __restrict__ x, long long ldx, const float* __res
 // ---------------------------------------------------------------- launches
 static int conv_threads(int vecs) { return vecs >= 128 ? 128 : (vecs + 31) / 32 * 32; }
 
-// Tokens per tile of the backward pass: 64 where that leaves enough threads, less
-// halo and fewer partial sums; at least 16; at most about 4096 partial sums.
+// Tokens per tile of the backward pass: 128 where that leaves 256 threads per SM,
+// less halo and fewer partial sums; else half, down to 8; at most about 4096 partial
+// sums.  Both sides, D = 2048, bf16, us: T = 1024 with tiles of 8/16/32/128 14.7,
+// 16.7, 21.4, 55.7; T = 4096 with 16/32/64 33.5, 28.7, 38.5; T = 16384 with
+// 32/64/128 102, 90, 84.
 static int conv_bwd_tile(long long tokens, int D)
 {
-    int r = 64;
-    while (r > 16 && (tokens / r) * (D / kV) < 148LL * 256) r /= 2;
+    int r = 128;
+    while (r > 8 && (tokens / r) * (D / kV) < 148LL * 256) r /= 2;
     while ((tokens + r - 1) / r > 4096) r *= 2;
     return r;
 }
@@ -487,10 +515,12 @@ static cudaError_t launch_conv_fwd(const ConvArgs& a, const void* s0, void* y, v
     const Seqs q{a.cu, a.nseq, a.T, a.tokens};
     const int nt = conv_threads(a.D / kV);
     const unsigned cb = (a.D / kV + nt - 1) / nt;
-    // Tokens per tile: long tiles re-read less halo, short ones give enough
-    // threads; at least ~1024 threads per SM while a tile keeps 16 tokens.
-    int R = 64;
-    while (R > 16 && (a.tokens / R) * cb * nt < 148LL * 1024) R /= 2;
+    // Tokens per tile: long tiles re-read less halo, short ones give enough threads:
+    // 32, halved to 8 until there are 256 threads per SM.  Both sides, D = 2048,
+    // bf16, us: T = 1024 with tiles of 8/16/32 4.4, 4.8, 6.8; T = 2048 7.8, 6.8, 8.7;
+    // T = 4096 11.7, 10.9, 10.5; T = 65536 139, 116, 109 (64: 108, 128: 115).
+    int R = 32;
+    while (R > 8 && (a.tokens / R) * cb * nt < 148LL * 256) R /= 2;
     const long long ntiles = (a.tokens + R - 1) / R;
     const bool apart = sT && sT == s0;   // in place: the states move after every tile has read them
     const long long gx = ntiles + (sT && !apart ? a.nseq : 0);
@@ -514,8 +544,10 @@ static cudaError_t launch_conv_step(const ConvArgs& a, void* state, void* y, cud
         conv_step_kernel<T, TO, W, SILU, RN><<<dim3((a.nseq + RN - 1) / RN, cb), nt, 0, st>>>(
             static_cast<const T*>(a.x), a.ldx, a.w, a.bias, static_cast<T*>(state), static_cast<TO*>(y), a.nseq, a.D);
     };
-    // four sequences per thread share its weights once that leaves 512 threads per SM
-    if ((long long)a.nseq / 4 * cb * nt >= 148LL * 512)
+    // four sequences per thread share its weights once that leaves 128 threads per SM
+    // (D = 4096, bf16, one against four: 16 sequences 1.85 / 2.18 us, 128 3.24 / 2.84,
+    // 1024 13.9 / 11.5)
+    if ((long long)a.nseq / 4 * cb * nt >= 148LL * 128)
         go(std::integral_constant<int, 4>{});
     else
         go(std::integral_constant<int, 1>{});

@@ -16,7 +16,7 @@ __device__ __forceinline__ float max_nan(float a, float b)
 
 // softplus(v) = max(v, 0) + log(1 + e), e = e^-|v|, of two values, to fp32 accuracy
 // for every v.  e: 2^(-|v| log2 e) with the rounding error of the exponent put back
-// (log2 e in two parts).  log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, without
+// (log2 e in two parts, as Cody and Waite reduce an argument).  log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, without
 // the cancellation of 1 + e; atanh(s) / s is a degree-4 polynomial in s^2 (largest
 // relative error 4e-9, fitted by reweighted least squares).
 __device__ __forceinline__ f32x2 softplus2(float v0, float v1)

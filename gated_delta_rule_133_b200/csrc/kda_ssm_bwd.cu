@@ -5,11 +5,14 @@
 //   dx_t = du_t Delta_t + skip dy0_t,   ddt_t = dDelta_t sigmoid(dt_t + bias)
 //   dz_t = gy_t y0_t silu'(z_t),   dh_0 = a_0 g_0
 // Four launches: the forward walk, which leaves the state before every CK-th token
-// and forms dz where it has y0 anyway;
-// the reverse walk, which recomputes CK states at a time into registers and runs
-// the reverse recurrence over them; and two sums
-// in a fixed order, of dB and dC over channel tiles and of dA, dskip and dbias
-// over the blocks that share a channel.
+// and forms dz where it has y0 anyway; the reverse walk, which recomputes CK states
+// at a time into registers and runs the reverse recurrence over them; and two sums
+// in a fixed order, of dB and dC over channel tiles and of dA, dskip and dbias over
+// the blocks that share a channel.
+//
+// 2 x 4096 tokens x 2048 channels, N = 16, bf16: 183 + 401 + 25 + 2 us.  The floor is
+// the exponentials, twice 72 us.  (dz and y0 in the reverse walk instead of the
+// forward one: 509 us for its 411 of that time.)
 #include "kda_sm100.cuh"
 #include "kda_ssm.cuh"
 
@@ -144,6 +147,13 @@ __device__ __forceinline__ void sum_channels(const f32x2 (&vb)[4], const f32x2 (
 // set), runs the chain g = C dy0 + a g', hands it on, and then forms everything
 // else.  Sums over a channel's lanes (dx, dDelta) and over a warp's channels (dB,
 // dC) are transposed reductions, many values at a time.
+//
+// Bound by issue: 30 instructions per warp and 32 (channel, state, token) in 63 % of
+// the slots, 8.8 words per lane of shared memory.  12 warps of 168 registers and 4
+// sets of 8 channels per warp: sums of dB and dC stay in registers over the sets (one
+// set per warp: 1115 us in all for 647), and are formed without selects (435 -> 411 us).
+// The warps take turns along one sequence, so a sequence of fewer than 8 W = 96 tokens
+// leaves some of them idle: 256 x 32 tokens x 1024 channels take 633 us.
 template <typename T, int N>
 __global__ void __launch_bounds__(Rev<N>::THREADS, 1)
 ssm_reverse_kernel(const BwdDev b)
@@ -425,8 +435,10 @@ ssm_reverse_kernel(const BwdDev b)
     }
 }
 
-// dB and dC of every token from the channel tiles' sums, a warp per (token,
-// group, 32 values).  Rows of no sequence: zero, here and in gx, gdt, gz.
+// dB and dC of every token from the channel tiles' sums, a warp per token.  Rows of
+// no sequence: zero, here and in gx, gdt, gz.  Bound by HBM: 67 MB of sums in 24 us
+// for 64 tiles of 8192 tokens (2.8 TB/s: 32 columns need only one load per tile and
+// lane, eight of them in flight).
 __global__ void __launch_bounds__(256)
 ssm_bwd_bc_kernel(const BwdDev b, float* __restrict__ gb, float* __restrict__ gc, int N)
 {
@@ -458,7 +470,7 @@ ssm_bwd_bc_kernel(const BwdDev b, float* __restrict__ gb, float* __restrict__ gc
     }
 }
 
-// dA, dskip, dbias over the slots.
+// dA, dskip, dbias over the slots: 2 us.
 __global__ void __launch_bounds__(256)
 ssm_bwd_params_kernel(const BwdDev b, float* __restrict__ gA, float* __restrict__ gskip, float* __restrict__ gbias, int N)
 {
@@ -479,7 +491,9 @@ ssm_bwd_params_kernel(const BwdDev b, float* __restrict__ gA, float* __restrict_
 constexpr long long kBwdTimeoutCycles = 1LL << 31;
 
 // Sequences are dealt to this many blocks per channel tile: enough to fill the
-// 148 SMs several times, few enough that the partial sums of dA stay small.
+// 148 SMs several times, few enough that the partial sums of dA stay small.  (64 x 64
+// tokens x 1024 channels with 2, 4, 16 times 148 blocks: 238, 221, 233 us; 256 x 32
+// tokens: 692, 633, 596.)
 static int bwd_slots(int nseq, int ntiles)
 {
     const int want = (148 * 4 + ntiles - 1) / ntiles;
