@@ -34,10 +34,11 @@ struct BwdDev {
 // warp holds a set of DT channels; it takes TK tokens at a time and does so for
 // the SETS sets of a tile of 32 channels one after the other, with the sums of dB
 // and dC over the channels in registers.  W warps take turns along the sequence.
-template <int N_>
+template <int N_, int W_ = N_ == 16 ? 12 : 8>
 struct Rev {
     static constexpr int N = N_, L = N == 16 ? 4 : 8, NPT = N / L, DT = 32 / L, TK = 32 / NPT, TILE = 32;
-    static constexpr int SETS = TILE / DT, W = N == 16 ? 12 : 8, THREADS = 32 * W;
+    static constexpr int SETS = TILE / DT, W = W_, THREADS = 32 * W;
+    static constexpr int BLOCKS = (N == 16 ? 12 : 8) / W;   // per SM
     static constexpr int VL = 2 * NPT / DT;                 // values of dB, dC of a token left to a lane
     static constexpr int EL = TK * DT / 2;                  // lanes with a pair of channels outside the walk
     static constexpr int DUROW = DT + 2, DYROW = DT + 2, SROW = 2 * DT, BQ = TK * N / 128;
@@ -152,13 +153,12 @@ __device__ __forceinline__ void sum_channels(const f32x2 (&vb)[4], const f32x2 (
 // the slots, 8.8 words per lane of shared memory.  12 warps of 168 registers and 4
 // sets of 8 channels per warp: sums of dB and dC stay in registers over the sets (one
 // set per warp: 1115 us in all for 647), and are formed without selects (435 -> 411 us).
-// The warps take turns along one sequence, so a sequence of fewer than 8 W = 96 tokens
-// leaves some of them idle: 256 x 32 tokens x 1024 channels take 633 us.
-template <typename T, int N>
-__global__ void __launch_bounds__(Rev<N>::THREADS, 1)
+// The warps take turns along one sequence; kNarrowTurns is about short ones.
+template <typename T, int N, int W_>
+__global__ void __launch_bounds__(Rev<N, W_>::THREADS, Rev<N, W_>::BLOCKS)
 ssm_reverse_kernel(const BwdDev b)
 {
-    using K = Rev<N>;
+    using K = Rev<N, W_>;
     constexpr int TK = K::TK, DT = K::DT, L = K::L, NPT = K::NPT, SETS = K::SETS, W = K::W, VL = K::VL, BQ = K::BQ;
     const SsmDev& p = b.p;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -490,14 +490,29 @@ ssm_bwd_params_kernel(const BwdDev b, float* __restrict__ gA, float* __restrict_
 // Budget of a wait for the next warp's state, in SM clock cycles (about a second).
 constexpr long long kBwdTimeoutCycles = 1LL << 31;
 
-// Sequences are dealt to this many blocks per channel tile: enough to fill the
-// 148 SMs several times, few enough that the partial sums of dA stay small.  (64 x 64
-// tokens x 1024 channels with 2, 4, 16 times 148 blocks: 238, 221, 233 us; 256 x 32
-// tokens: 692, 633, 596.)
-static int bwd_slots(int nseq, int ntiles)
+// Turns along one sequence leave warps idle where it has few of them.  So up to
+// kNarrowTurns rounds of turns, where the sequences fill the SMs all the same, a block
+// has four warps, and an SM three (N = 16) or two of these.  All four launches,
+// D = 1024, bf16, 12 or 8 warps against 4, us: N = 16, 256 x 32 tokens 633 / 395,
+// 64 x 96 279 / 247, 32 x 256 303 / 309, 16 x 1024 591 / 670; N = 32, 64 x 64 340 / 307,
+// 32 x 256 552 / 572; N = 64, 64 x 64 791 / 728, 32 x 256 1368 / 1425.
+constexpr int kNarrowTurns = 2;
+
+// Sequences are dealt to `slots` blocks per channel tile: enough to fill the 148 SMs
+// several times, few enough that the partial sums of dA stay small.  (64 x 64 tokens x
+// 1024 channels with 2, 4, 16 times 148 blocks of 12 warps: 238, 221, 233 us.)
+struct BwdShape {
+    bool narrow;
+    int slots;
+};
+static BwdShape bwd_shape(int nseq, long long tokens, int ntiles, int N)
 {
-    const int want = (148 * 4 + ntiles - 1) / ntiles;
-    return nseq < want ? nseq : want;
+    const int wide = N == 16 ? 12 : 8, per_sm = wide / 4, tk = N == 64 ? 4 : 8;
+    BwdShape s;
+    s.narrow = tokens / nseq <= kNarrowTurns * wide * tk && (long long)nseq * ntiles >= 148LL * per_sm;
+    const int want = (148 * 4 * (s.narrow ? per_sm : 1) + ntiles - 1) / ntiles;
+    s.slots = nseq < want ? nseq : want;
+    return s;
 }
 
 struct BwdWorkspace {
@@ -508,7 +523,7 @@ template <int N>
 static BwdWorkspace bwd_layout(int nseq, int T, long long tokens, int D, int G, bool varlen)
 {
     using K = Rev<N>;
-    const int tiles = (D / G + K::TILE - 1) / K::TILE, slots = bwd_slots(nseq, tiles * G);
+    const int tiles = (D / G + K::TILE - 1) / K::TILE, slots = bwd_shape(nseq, tokens, tiles * G, N).slots;
     const size_t blocks = varlen ? (size_t)(tokens / K::TK) + nseq : (size_t)nseq * ((T + K::TK - 1) / K::TK);
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     BwdWorkspace w;
@@ -518,6 +533,19 @@ static BwdWorkspace bwd_layout(int nseq, int T, long long tokens, int D, int G, 
     w.partv = w.partA + up((size_t)slots * D * N * 4);
     w.total = w.partv + up((size_t)slots * 2 * D * 4);
     return w;
+}
+
+template <typename T, int N, int W>
+static cudaError_t launch_reverse(const BwdDev& b, cudaStream_t s)
+{
+    using K = Rev<N, W>;
+    constexpr size_t smem = K::template smem<T>();
+    static_assert(smem <= 227 * 1024 && K::BLOCKS * (smem + 1024) <= 228 * 1024, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(ssm_reverse_kernel<T, N, W>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    ssm_reverse_kernel<T, N, W><<<(unsigned)(b.slots * b.p.tiles * b.p.G), K::THREADS, smem, s>>>(b);
+    return cudaGetLastError();
 }
 
 template <typename T, int N>
@@ -535,15 +563,14 @@ static cudaError_t launch_bwd(const SsmArgs& a, const SsmGrads& g, void* ws, cud
     b.partA = reinterpret_cast<float*>(base + w.partA);
     b.partv = reinterpret_cast<float*>(base + w.partv);
     b.p.tiles = (a.D / a.G + K::TILE - 1) / K::TILE;
-    b.slots = bwd_slots(a.nseq, b.p.tiles * a.G);
+    const BwdShape shape = bwd_shape(a.nseq, a.tokens, b.p.tiles * a.G, N);
+    b.slots = shape.slots;
     b.timeout_cycles = kBwdTimeoutCycles;
     cudaError_t e = launch_walk<T, N, K::TK>(a, b.p, s,
                                                     WalkBwd{g.gy, g.gz, reinterpret_cast<float*>(base + w.ckpt)});
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(ssm_reverse_kernel<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)K::template smem<T>());
+    e = shape.narrow ? launch_reverse<T, N, 4>(b, s) : launch_reverse<T, N, K::W>(b, s);
     if (e != cudaSuccess) return e;
-    ssm_reverse_kernel<T, N><<<(unsigned)(b.slots * b.p.tiles * a.G), K::THREADS, K::template smem<T>(), s>>>(b);
     ssm_bwd_bc_kernel<<<(unsigned)((a.tokens + 7) / 8), 256, 0, s>>>(b, g.gb, g.gc, N);
     ssm_bwd_params_kernel<<<(unsigned)(((long long)a.D * (N + 2) + 255) / 256), 256, 0, s>>>(b, g.gA, g.gskip,
                                                                                              g.gdt_bias, N);

@@ -211,6 +211,21 @@ def test_ssm_many_sequences():
     _check_bwd(p, cu, grads, gy, gsT)
 
 
+@pytest.mark.parametrize("S,G,dtype", [(16, 1, torch.bfloat16), (32, 3, torch.float32), (64, 1, torch.bfloat16)])
+def test_ssm_bwd_of_many_short_sequences(S, G, dtype):
+    """Blocks of four warps, several sequences each: lengths of less than one turn, of
+    many rounds of turns and of zero, a channel tile that is not full."""
+    lens = [(13 * i) % 9 for i in range(450)]
+    lens[7], lens[300] = 150, 33
+    p, cu, gy, gsT = _inputs(lens, 264, S, G, dtype, 46)
+    d, cud = _dev(p), torch.from_numpy(cu).to(DEV)
+    grads = _bwd(d, gy.to(DEV), gsT.to(DEV), cud)
+    again = _bwd(d, gy.to(DEV), gsT.to(DEV), cud)
+    kda.kda_check()
+    _check_bwd(p, cu, grads, gy, gsT)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
 def test_ssm_backward_without_softplus():
     p, cu, gy, gsT = _inputs([40, 7], 32, 16, 2, torch.float32, 5)
     p["dt"], p["dt_bias"] = p["dt"].abs() * 0.1, p["dt_bias"].abs() * 0.1
