@@ -112,9 +112,10 @@ __device__ __forceinline__ void put(TO* y, const f32x2 (&p)[2])
 }
 
 // Grid: x = token tiles of R tokens, then (if sT) one block per sequence for
-// the final states; y = channel blocks.  U tokens are loaded while the U before
-// them are summed (16384 x 2048: 31.4 us; loaded and summed in turn, six blocks per
-// SM instead of five: 32.7; U = 4: 30.7, but 11.5 instead of 10.1 at 4096 x 2048).
+// the final states; y = channel blocks.  A token is loaded U tokens before it is
+// summed (16384 x 2048: 31.5 us; U loaded, then summed, six blocks per SM instead of
+// five: 32.7; U = 8 with six or seven blocks 33.9, 35.8, U = 4 with eight 32.4, but
+// 11.9 instead of 10.2 at 4096 x 2048).
 template <typename T, typename TO, int W, bool SILU>
 __global__ void __launch_bounds__(128, 5)
 conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ bias,
@@ -177,13 +178,12 @@ conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
             for (int u = 0; u < U; ++u, px += ldx) next[u] = *reinterpret_cast<const Quad*>(px);
 #pragma unroll 1
             for (; n >= 2 * U; n -= U) {
-                Quad raw[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) raw[u] = next[u];
-#pragma unroll
-                for (int u = 0; u < U; ++u, px += ldx) next[u] = *reinterpret_cast<const Quad*>(px);
-#pragma unroll
-                for (int u = 0; u < U; ++u) step(raw[u]);
+                for (int u = 0; u < U; ++u, px += ldx) {
+                    const Quad raw = next[u];
+                    next[u] = *reinterpret_cast<const Quad*>(px);
+                    step(raw);
+                }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) step(next[u]);
@@ -249,17 +249,19 @@ conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict
 // kernel adds in a fixed order: no atomics, the same result every time.
 //
 // Ten bytes per element (x in bf16, gy, gx in fp32), so HBM is the bound; what it
-// reaches is set by the loads in flight, four blocks of 128 registers per SM.
-// 8192 x 2048: 44 + 4 us, 3.8 TB/s.  Two channels per thread 47 us and more; tiles
-// staged in shared memory by cp.async, two channels per thread, 45.5; U = 2, 6, 8 and
-// five to eight blocks per SM slower; channel blocks first in the grid 69.
+// reaches is set by the loads in flight: four blocks of 128 registers per SM, and
+// every token's loads issued U tokens before they are used.  Both kernels: 8192 x 2048
+// 44 us, 3.8 TB/s; 65536 x 2048 271 us, 4.9 TB/s (with loads and sums in turn 48 and
+// 313; without the bound of 128 registers 56 and 280; five blocks 82 and 476).  Two
+// channels per thread, tiles staged in shared memory by cp.async, and channel blocks
+// first in the grid measured slower.
 template <typename T, int W, bool SILU>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 4)
 conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ bias,
                 const T* __restrict__ s0, const float* __restrict__ gy, const float* __restrict__ gsT,
                 float* __restrict__ gx, float* __restrict__ part, Seqs q, int D, int R)
 {
-    constexpr int U = 4;
+    constexpr int U = sizeof(T) == 2 ? 4 : 3;   // tokens loaded ahead: 24 registers
     typedef typename Raw<T>::quad Quad;
     flag_bad_sequences(q);
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kV;
@@ -359,14 +361,27 @@ conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
             slope(*reinterpret_cast<const Quad*>(px), *reinterpret_cast<const float4*>(pg), true, d);
             shift(d);
         }
-#pragma unroll 1
-        for (; n >= U; n -= U) {
+        if (n >= U) {
             Quad raw[U];
             float4 g[U];
 #pragma unroll
             for (int u = 0; u < U; ++u, px += ldx, pg += D) {
                 raw[u] = *reinterpret_cast<const Quad*>(px);
                 g[u] = *reinterpret_cast<const float4*>(pg);
+            }
+#pragma unroll 1
+            for (; n >= 2 * U; n -= U) {
+#pragma unroll
+                for (int u = 0; u < U; ++u, px += ldx, pg += D) {
+                    const Quad r0 = raw[u];
+                    const float4 g0 = g[u];
+                    raw[u] = *reinterpret_cast<const Quad*>(px);
+                    g[u] = *reinterpret_cast<const float4*>(pg);
+                    slope(r0, g0, true, d);
+                    input_grad(d, o);
+                    shift(d);
+                    emit(o);
+                }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -375,6 +390,7 @@ conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
                 shift(d);
                 emit(o);
             }
+            n -= U;
         }
 #pragma unroll 1
         for (; n > 0; --n, px += ldx, pg += D) {
@@ -500,7 +516,7 @@ static int conv_threads(int vecs) { return vecs >= 128 ? 128 : (vecs + 31) / 32 
 // less halo and fewer partial sums; else half, down to 8; at most about 4096 partial
 // sums.  Both sides, D = 2048, bf16, us: T = 1024 with tiles of 8/16/32/128 14.7,
 // 16.7, 21.4, 55.7; T = 4096 with 16/32/64 33.5, 28.7, 38.5; T = 16384 with
-// 32/64/128 102, 90, 84.
+// 32/64/128 102, 90, 84 (all of them 0 to 12 % less since loads are issued ahead).
 static int conv_bwd_tile(long long tokens, int D)
 {
     int r = 128;
