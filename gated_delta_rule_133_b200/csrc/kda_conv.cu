@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(128, 5)
 conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ bias,
                 const T* s0, TO* __restrict__ y, T* sT, Seqs q, int D, int R, int ntiles)
 {
-    constexpr int U = 8;
+    constexpr int U = sizeof(T) == 2 ? 8 : 4;   // 16 registers; fp32 with 8: 65536 x 2048 206 us for 175 (spills)
     typedef typename Raw<T>::quad Quad;
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kV;
     if ((int)blockIdx.x >= ntiles) {
@@ -261,7 +261,7 @@ conv_bwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
                 const T* __restrict__ s0, const float* __restrict__ gy, const float* __restrict__ gsT,
                 float* __restrict__ gx, float* __restrict__ part, Seqs q, int D, int R)
 {
-    constexpr int U = sizeof(T) == 2 ? 4 : 3;   // tokens loaded ahead: 24 registers
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;   // tokens ahead; fp32 with 3: 8192 x 2048 54 us for 50 (spills)
     typedef typename Raw<T>::quad Quad;
     flag_bad_sequences(q);
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kV;
