@@ -65,6 +65,7 @@ SIGNATURES = {
     "kda_ssm_varlen_bwd_workspace_size": (_I, [_I] * 6 + [_ZP]),
     "kda_check": (_I, [_P]),
     "kda_selftest_timeout": (_I, [ctypes.c_longlong, _P]),
+    "kda_selftest_scan_timeout": (_I, [ctypes.c_longlong, _P, _Z, _P]),
     "kda_status_string": (ctypes.c_char_p, [_I]),
     "kda_version": (_I, []),
 }

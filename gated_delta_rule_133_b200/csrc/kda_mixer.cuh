@@ -296,5 +296,7 @@ struct SsmGrads {
 };
 size_t ssm_bwd_workspace(int nseq, int T, long long tokens, int D, int N, int G, bool varlen);
 cudaError_t ssm_bwd(const SsmArgs& a, const SsmGrads& g, void* ws, cudaStream_t s);
+size_t ssm_bwd_selftest_workspace();
+cudaError_t ssm_bwd_selftest(long long limit_cycles, void* ws, cudaStream_t s);
 
 }  // namespace kda

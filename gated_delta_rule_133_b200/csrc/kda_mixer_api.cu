@@ -335,4 +335,12 @@ kda_status kda_ssm_varlen_bwd_workspace_size(int N, int T, int D, int S, int G, 
     return KDA_OK;
 }
 
+kda_status kda_selftest_scan_timeout(long long limit_cycles, void* workspace, size_t workspace_bytes_, void* stream)
+{
+    if (limit_cycles < 1 || limit_cycles > (1LL << 32)) return KDA_ERR_INVALID_ARG;
+    const kda_status st = check_workspace(workspace, workspace_bytes_, kda::ssm_bwd_selftest_workspace());
+    if (st != KDA_OK) return st;
+    return from_cuda(kda::ssm_bwd_selftest(limit_cycles, workspace, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

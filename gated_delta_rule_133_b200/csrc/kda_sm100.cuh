@@ -85,6 +85,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     return false;
 }
 
+// mbar_wait by a whole warp, with one answer for all its lanes.  Every lane polls
+// and gives up for itself (the phase may complete, or *abort be set, between two
+// lanes' polls), so a branch on mbar_wait's own result could split the warp in
+// front of its next full-mask operation.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                               long long limit_cycles)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_cycles));
+}
+
 // ---------------------------------------------------------------- TMA / proxies
 __device__ __forceinline__ void fence_proxy_async()
 {

@@ -27,6 +27,7 @@ struct BwdDev {
     float *part;              // [tile of the group][token][G][2 N]: dB, dC
     float *partA, *partv;     // [slot][D][N]; [slot][2][D]: dskip, dbias
     int slots;
+    int arrivals;             // that complete a hand-over: 1 (2 in the self-test: none ever completes)
     long long timeout_cycles;
 };
 
@@ -198,7 +199,7 @@ ssm_reverse_kernel(const BwdDev b)
         sBias[threadIdx.x] = in && p.dt_bias ? p.dt_bias[c00 + threadIdx.x] : 0.f;
         sSkip[threadIdx.x] = in && p.skip ? p.skip[c00 + threadIdx.x] : 0.f;
     }
-    if (threadIdx.x < W * SETS) sm100::mbar_init(bars + threadIdx.x, 1);
+    if (threadIdx.x < W * SETS) sm100::mbar_init(bars + threadIdx.x, b.arrivals);
     if (threadIdx.x == 0) {
         *aborted = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -316,7 +317,7 @@ ssm_reverse_kernel(const BwdDev b)
                 }
                 f32x2 cr[NPT / 2];
                 if (r > 0) {
-                    ok = sm100::mbar_wait(bars + from * SETS + o, parity, aborted, b.timeout_cycles);
+                    ok = sm100::mbar_wait_warp(bars + from * SETS + o, parity, aborted, b.timeout_cycles);
                     if (!ok) break;
                     read_states(sCarry + ((from * SETS + o) * 32 + lane) * NPT, cr);
                 } else {
@@ -565,6 +566,7 @@ static cudaError_t launch_bwd(const SsmArgs& a, const SsmGrads& g, void* ws, cud
     b.p.tiles = (a.D / a.G + K::TILE - 1) / K::TILE;
     const BwdShape shape = bwd_shape(a.nseq, a.tokens, b.p.tiles * a.G, N);
     b.slots = shape.slots;
+    b.arrivals = 1;
     b.timeout_cycles = kBwdTimeoutCycles;
     cudaError_t e = launch_walk<T, N, K::TK>(a, b.p, s,
                                                     WalkBwd{g.gy, g.gz, reinterpret_cast<float*>(base + w.ckpt)});
@@ -577,7 +579,49 @@ static cudaError_t launch_bwd(const SsmArgs& a, const SsmGrads& g, void* ws, cud
     return cudaGetLastError();
 }
 
+// The reverse walk over one sequence of kTestTokens tokens and one tile of channels,
+// all zeros, with every hand-over withheld: each warp's wait runs out, and the block
+// leaves through its common exit.
+constexpr int kTestTokens = 100, kTestD = 32, kTestN = 16;
+constexpr int kTestZeros = (kTestTokens / 8 + 1) * kTestD * kTestN;   // floats of any input, the states the longest
+
+template <int W>
+static cudaError_t launch_reverse_withheld(float* ws, long long limit_cycles, cudaStream_t s)
+{
+    BwdDev b{};
+    float* out = ws + kTestZeros;
+    b.p.x = b.p.dt = b.p.b = b.p.c = b.p.A = b.gy = b.ckpt = ws;
+    b.p.ldx = b.p.lddt = 4 * kTestD;
+    b.p.ldb = b.p.ldc = 4 * kTestN;
+    b.p.q = Seqs{nullptr, 1, kTestTokens, kTestTokens};
+    b.p.D = kTestD;
+    b.p.G = b.p.tiles = b.slots = 1;
+    b.gx = out; out += kTestTokens * kTestD;
+    b.gdt = out; out += kTestTokens * kTestD;
+    b.part = out; out += kTestTokens * 2 * kTestN;
+    b.partA = out; out += kTestD * kTestN;
+    b.partv = out;
+    b.arrivals = 2;
+    b.timeout_cycles = limit_cycles;
+    return launch_reverse<float, kTestN, W>(b, s);
+}
+
 }  // namespace mixer
+
+size_t ssm_bwd_selftest_workspace()
+{
+    using namespace mixer;
+    return sizeof(float) * (kTestZeros + kTestTokens * 2 * (kTestD + kTestN) + kTestD * (kTestN + 2));
+}
+
+cudaError_t ssm_bwd_selftest(long long limit_cycles, void* ws, cudaStream_t s)
+{
+    float* f = static_cast<float*>(ws);
+    cudaError_t e = cudaMemsetAsync(f, 0, mixer::kTestZeros * sizeof(float), s);
+    if (e == cudaSuccess) e = mixer::launch_reverse_withheld<mixer::Rev<mixer::kTestN>::W>(f, limit_cycles, s);
+    if (e == cudaSuccess) e = mixer::launch_reverse_withheld<4>(f, limit_cycles, s);
+    return e;
+}
 
 size_t ssm_bwd_workspace(int nseq, int T, long long tokens, int D, int N, int G, bool varlen)
 {

@@ -535,6 +535,15 @@ kda_status kda_check(void* stream);
  */
 kda_status kda_selftest_timeout(long long limit_cycles, void* stream);
 
+/*
+ * The same for the waits between the warps of the selective scan's backward
+ * pass: its reverse walk runs over a small sequence of zeros with every hand-over
+ * withheld, in both of its block sizes, one after the other.  Every wait gives
+ * up after `limit_cycles` and each launch exits normally.
+ *   workspace  device scratch of at least 128 KiB, 256-byte aligned
+ */
+kda_status kda_selftest_scan_timeout(long long limit_cycles, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* kda_status_string(kda_status status);
 
