@@ -124,11 +124,11 @@ conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
     constexpr int U = sizeof(T) == 2 ? 8 : 4;   // 16 registers; fp32 with 8: 65536 x 2048 206 us for 175 (spills)
     typedef typename Raw<T>::quad Quad;
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kV;
+    flag_bad_sequences(q);   // by every block: the sequences are dealt to the whole grid
     if ((int)blockIdx.x >= ntiles) {
         if (c < D) write_state<T, W>(x, ldx, s0, sT, q, blockIdx.x - ntiles, D, c);
         return;
     }
-    flag_bad_sequences(q);
     long long t = (long long)blockIdx.x * R;
     const long long t1 = min(t + R, q.tokens);
     int i = max(find_sequence(q, t), 0);
