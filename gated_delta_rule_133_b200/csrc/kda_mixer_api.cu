@@ -17,17 +17,44 @@ bool valid_ld(long long ld, long long row, kda_dtype dtype)
 
 bool opt_aligned16(const void* p) { return !p || aligned16(p); }
 
-// Whether rows of `row` elements, `ld` apart, and the dense output y [tokens, D]
-// share memory: an output written while other blocks still read the input.
-bool overlaps(const void* in, long long ld, long long row, kda_dtype dtype, const void* y, long long D,
-              kda_dtype o_dtype, long long tokens)
+// Memory that a call reads or writes.
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+
+size_t elem_size(kda_dtype dtype) { return dtype == KDA_BF16 ? 2 : 4; }
+
+// `tokens` rows of `row` elements, `ld` apart (what lies between them counts).
+Span rows(const void* p, long long ld, long long row, long long tokens, kda_dtype dtype)
 {
-    if (!in || tokens == 0) return false;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(y);
-    const uintptr_t na = (uintptr_t)((tokens - 1) * ld + row) * (dtype == KDA_BF16 ? 2 : 4);
-    const uintptr_t nb = (uintptr_t)(tokens * D) * (o_dtype == KDA_BF16 ? 2 : 4);
-    return a < b + nb && b < a + na;
+    return Span{p, tokens > 0 ? (size_t)((tokens - 1) * ld + row) * elem_size(dtype) : 0};
 }
+
+Span floats(const float* p, long long n) { return Span{p, (size_t)n * sizeof(float)}; }
+
+bool overlap(const Span& a, const Span& b)
+{
+    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y + b.bytes && y < x + a.bytes;
+}
+
+// Whether an output shares memory with an input or with another output: blocks
+// write it while others still read.
+template <int NO, int NI>
+bool any_overlap(const Span (&out)[NO], const Span (&in)[NI])
+{
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return true;
+        for (int j = 0; j < NI; ++j)
+            if (overlap(out[i], in[j])) return true;
+    }
+    return false;
+}
+
+Span bounds(const int32_t* cu, int nseq) { return Span{cu, cu ? (size_t)(nseq + 1LL) * sizeof(int32_t) : 0}; }
 
 kda_status check_conv(const kda::ConvArgs& a, const void* y, const void* s0, const void* sT, int mode)
 {
@@ -63,16 +90,24 @@ kda_status check_cu(const int32_t* cu, int N, int T)
     return KDA_OK;
 }
 
+// The state may be updated in place: s0 == sT counts as the output alone.
+bool conv_overlap(const kda::ConvArgs& a, const void* s0, const void* y, const void* sT, kda_dtype o_dtype)
+{
+    const size_t state = (size_t)a.nseq * (a.W - 1) * a.D * elem_size(a.dtype);
+    const Span out[] = {rows(y, a.D, a.D, a.tokens, o_dtype), {sT, state}};
+    const Span in[] = {rows(a.x, a.ldx, a.D, a.tokens, a.dtype), floats(a.w, (long long)a.D * a.W),
+                       floats(a.bias, a.D), bounds(a.cu, a.nseq), {s0 == sT ? nullptr : s0, state}};
+    return any_overlap(out, in);
+}
+
 kda_status conv_fwd_call(const kda::ConvArgs& a, const void* s0, void* y, void* sT, kda_dtype o_dtype, int mode,
                          void* stream)
 {
     const kda_status st = check_conv(a, y, s0, sT, mode);
     if (st != KDA_OK) return st;
-    if (!valid_dtype(o_dtype) || overlaps(a.x, a.ldx, a.D, a.dtype, y, a.D, o_dtype, a.tokens))
-        return KDA_ERR_INVALID_ARG;
+    if (!valid_dtype(o_dtype) || conv_overlap(a, s0, y, sT, o_dtype)) return KDA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const size_t es = a.dtype == KDA_BF16 ? 2 : 4;
-    if (a.tokens == 0) return copy_bytes(s0, sT, (size_t)a.nseq * (a.W - 1) * a.D * es, s);
+    if (a.tokens == 0) return copy_bytes(s0, sT, (size_t)a.nseq * (a.W - 1) * a.D * elem_size(a.dtype), s);
     return from_cuda(kda::conv_fwd(a, s0, y, sT, o_dtype, s));
 }
 
@@ -83,6 +118,16 @@ kda_status conv_bwd_call(const kda::ConvArgs& a, const void* s0, const float* gy
     if (st != KDA_OK) return st;
     if (!gw || !aligned16(gw) || !opt_aligned16(gb) || !opt_aligned16(gs0)) return KDA_ERR_INVALID_ARG;
     if (a.tokens > 0 && (!gy || !aligned16(gy))) return KDA_ERR_INVALID_ARG;
+    const size_t need = a.tokens == 0 ? 0 : kda::conv_bwd_workspace(a.tokens, a.D, a.W);
+    st = check_workspace(ws, ws_bytes, need);
+    if (st != KDA_OK) return st;
+    const long long act = a.tokens * a.D, state = (long long)a.nseq * (a.W - 1) * a.D;
+    const Span out[] = {floats(gx, act), floats(gw, (long long)a.D * a.W), floats(gb, a.D), floats(gs0, state),
+                        {ws, need}};
+    const Span in[] = {rows(a.x, a.ldx, a.D, a.tokens, a.dtype), floats(a.w, (long long)a.D * a.W),
+                       floats(a.bias, a.D), bounds(a.cu, a.nseq), {s0, (size_t)state * elem_size(a.dtype)},
+                       floats(gy, act), floats(gsT, state)};
+    if (any_overlap(out, in)) return KDA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.tokens == 0) {
         st = copy_bytes(nullptr, gw, (size_t)a.D * a.W * 4, s);
@@ -90,8 +135,6 @@ kda_status conv_bwd_call(const kda::ConvArgs& a, const void* s0, const float* gy
         if (st == KDA_OK) st = copy_bytes(gsT, gs0, (size_t)a.nseq * (a.W - 1) * a.D * 4, s);
         return st;
     }
-    st = check_workspace(ws, ws_bytes, kda::conv_bwd_workspace(a.tokens, a.D, a.W));
-    if (st != KDA_OK) return st;
     return from_cuda(kda::conv_bwd(a, s0, gy, gsT, gx, gw, gb, gs0, ws, s));
 }
 
@@ -124,21 +167,31 @@ kda_status check_ssm(const kda::SsmArgs& a, const void* y, int mode)
     return a.tokens > kMaxTokens ? KDA_ERR_UNSUPPORTED : KDA_OK;
 }
 
-bool ssm_overlap(const kda::SsmArgs& a, const void* y, kda_dtype o_dtype)
+// The inputs of a scan; `s0` where it is read and not also written.
+struct SsmSpans {
+    Span in[10];
+};
+SsmSpans ssm_inputs(const kda::SsmArgs& a, const float* s0)
 {
     const long long gs = (long long)a.G * a.N;
-    auto hit = [&](const void* in, long long ld, long long row) {
-        return overlaps(in, ld, row, a.dtype, y, a.D, o_dtype, a.tokens);
-    };
-    return hit(a.x, a.ldx, a.D) || hit(a.dt, a.lddt, a.D) || hit(a.b, a.ldb, gs) || hit(a.c, a.ldc, gs) ||
-           hit(a.z, a.ldz, a.D);
+    return SsmSpans{{rows(a.x, a.ldx, a.D, a.tokens, a.dtype), rows(a.dt, a.lddt, a.D, a.tokens, a.dtype),
+                     rows(a.b, a.ldb, gs, a.tokens, a.dtype), rows(a.c, a.ldc, gs, a.tokens, a.dtype),
+                     rows(a.z, a.ldz, a.D, a.tokens, a.dtype), floats(a.A, (long long)a.D * a.N), floats(a.skip, a.D),
+                     floats(a.dt_bias, a.D), bounds(a.cu, a.nseq), floats(s0, (long long)a.nseq * a.D * a.N)}};
+}
+
+// The state may be updated in place: s0 == sT counts as the output alone.
+bool ssm_overlap(const kda::SsmArgs& a, const void* y, const float* sT, kda_dtype o_dtype)
+{
+    const Span out[] = {rows(y, a.D, a.D, a.tokens, o_dtype), floats(sT, (long long)a.nseq * a.D * a.N)};
+    return any_overlap(out, ssm_inputs(a, a.s0 == sT ? nullptr : a.s0).in);
 }
 
 kda_status ssm_fwd_call(const kda::SsmArgs& a, void* y, float* sT, kda_dtype o_dtype, int mode, void* stream)
 {
     const kda_status st = check_ssm(a, y, mode);
     if (st != KDA_OK) return st;
-    if (!valid_dtype(o_dtype) || !opt_aligned16(sT) || ssm_overlap(a, y, o_dtype)) return KDA_ERR_INVALID_ARG;
+    if (!valid_dtype(o_dtype) || !opt_aligned16(sT) || ssm_overlap(a, y, sT, o_dtype)) return KDA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.tokens == 0) return copy_state(a.s0, sT, (size_t)a.nseq * a.D * a.N, s);
     return from_cuda(kda::ssm_fwd(a, y, sT, o_dtype, s));
@@ -158,6 +211,16 @@ kda_status ssm_bwd_call(const kda::SsmArgs& a, const kda::SsmGrads& g, int mode,
         if (!aligned16(g.gy) || !aligned16(g.gdt) || !aligned16(g.gb) || !aligned16(g.gc) || !opt_aligned16(g.gz))
             return KDA_ERR_INVALID_ARG;
     }
+    const size_t need =
+        a.tokens == 0 ? 0 : kda::ssm_bwd_workspace(a.nseq, a.T, a.tokens, a.D, a.N, a.G, varlen);
+    st = check_workspace(ws, ws_bytes, need);
+    if (st != KDA_OK) return st;
+    const long long act = a.tokens * a.D, bc = a.tokens * a.G * a.N, state = (long long)a.nseq * a.D * a.N;
+    const Span out[] = {floats(g.gx, act), floats(g.gdt, act), floats(g.gA, (long long)a.D * a.N), floats(g.gb, bc),
+                        floats(g.gc, bc), floats(g.gskip, a.D), floats(g.gz, act), floats(g.gdt_bias, a.D),
+                        floats(g.gs0, state), {ws, need}};
+    const Span grads[] = {floats(g.gy, act), floats(g.gsT, state)};
+    if (any_overlap(out, ssm_inputs(a, a.s0).in) || any_overlap(out, grads)) return KDA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.tokens == 0) {
         st = copy_bytes(nullptr, g.gA, (size_t)a.D * a.N * 4, s);
@@ -166,8 +229,6 @@ kda_status ssm_bwd_call(const kda::SsmArgs& a, const kda::SsmGrads& g, int mode,
         if (st == KDA_OK) st = copy_state(g.gsT, g.gs0, (size_t)a.nseq * a.D * a.N, s);
         return st;
     }
-    st = check_workspace(ws, ws_bytes, kda::ssm_bwd_workspace(a.nseq, a.T, a.tokens, a.D, a.N, a.G, varlen));
-    if (st != KDA_OK) return st;
     return from_cuda(kda::ssm_bwd(a, g, ws, s));
 }
 
@@ -202,7 +263,7 @@ kda_status kda_conv_step(const void* x, long long ldx, const float* weight, cons
     const kda::ConvArgs a = conv_args(x, ldx, weight, bias, nullptr, N, 1, N, D, W, dtype, mode);
     const kda_status st = check_conv(a, y, state, nullptr, mode);
     if (st != KDA_OK) return st;
-    if (!valid_dtype(o_dtype) || (N > 0 && !state) || overlaps(x, ldx, D, dtype, y, D, o_dtype, N))
+    if (!valid_dtype(o_dtype) || (N > 0 && !state) || conv_overlap(a, nullptr, y, state, o_dtype))
         return KDA_ERR_INVALID_ARG;
     if (N == 0) return KDA_OK;
     return from_cuda(kda::conv_step(a, state, y, o_dtype, static_cast<cudaStream_t>(stream)));
@@ -274,7 +335,7 @@ kda_status kda_ssm_step(const void* x, long long ldx, const void* dt, long long 
                          N, D, S, G, (mode & KDA_SSM_SOFTPLUS) != 0, dtype};
     const kda_status st = check_ssm(a, y, mode);
     if (st != KDA_OK) return st;
-    if (!valid_dtype(o_dtype) || (N > 0 && (!state || !aligned16(state))) || ssm_overlap(a, y, o_dtype))
+    if (!valid_dtype(o_dtype) || (N > 0 && (!state || !aligned16(state))) || ssm_overlap(a, y, state, o_dtype))
         return KDA_ERR_INVALID_ARG;
     if (N == 0) return KDA_OK;
     return from_cuda(kda::ssm_step(a, state, y, o_dtype, static_cast<cudaStream_t>(stream)));

@@ -12,6 +12,8 @@ and their gradients (``*_bwd``).  As in the rest of the package these functions
 only check arguments, allocate outputs and pass pointers; the token-major inputs
 (x, dt, B, C, z) may be column slices of wider tensors (last dimension
 contiguous, one stride from token to token), every other tensor is contiguous.
+An output (y, a state, the workspace) that shares memory with an input or another
+output is refused; a final state may be the initial state itself.
 All tensors are on one CUDA device; the work runs on ``stream``, or on that
 device's current stream, and new tensors belong to that stream.
 """

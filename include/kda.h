@@ -359,6 +359,15 @@ kda_status kda_dplr_varlen_fwd_workspace_size(int N, int T, int H, int dk, int d
                                               size_t* bytes);
 
 /*
+ * Shared memory, for the convolution and the scan below: what a call writes
+ * (y, states, gradients, workspace) must not share memory with what it reads or
+ * with another of its outputs, or it returns KDA_ERR_INVALID_ARG.  Ranges of
+ * addresses are compared; rows that lie apart count with what is between them.
+ * The one exception: a final state may be the initial state's memory, whole and
+ * in the same order.
+ */
+
+/*
  * Short causal depthwise convolution, the token mixer in front of the layer's
  * q, k, v projections and of the selective scan below.  Per channel d:
  *
@@ -375,8 +384,7 @@ kda_status kda_dplr_varlen_fwd_workspace_size(int N, int T, int H, int dk, int d
  *   weight   [D, W] fp32; bias [D] fp32 or NULL; 16-byte aligned
  *   initial_state / final_state [N, W - 1, D] of type `dtype` or NULL (final may
  *            be the same memory as initial); copies of inputs, never rounded
- *   y        [B, T, D] (dense) or [T, D] (packed), o_dtype, written; must not
- *            share memory with x (KDA_ERR_INVALID_ARG)
+ *   y        [B, T, D] (dense) or [T, D] (packed), o_dtype, written
  *   mode     0 or KDA_CONV_SILU
  * D a multiple of 8, at most 2^20, W in {2, 3, 4}: others return
  * KDA_ERR_UNSUPPORTED.  Packed batches follow kda_varlen_fwd's rules: a sequence
@@ -407,8 +415,7 @@ kda_status kda_conv_step(const void* x, long long ldx, const float* weight, cons
  *   workspace  at least kda_conv_bwd_workspace_size() bytes, 256-byte aligned
  *              (partial sums of the weight's gradient, added in a fixed order)
  * Packed batches: rows of no sequence and of skipped ones get a zero grad_x, a
- * skipped sequence's grad_initial_state is grad_final_state.  The gradient
- * buffers must not alias the inputs.
+ * skipped sequence's grad_initial_state is grad_final_state.
  */
 kda_status kda_conv_bwd(const void* x, long long ldx, const float* weight, const float* bias,
                         const void* initial_state, const float* grad_y, const float* grad_final_state,
@@ -446,8 +453,7 @@ kda_status kda_conv_bwd_workspace_size(long long tokens, int D, int W, size_t* b
  *              them, count as -1e30, so that a step size of zero keeps the state); skip, dt_bias [D] fp32 or NULL
  *   initial_state / final_state [N, D, S] fp32 or NULL (final may be the same
  *              memory as initial)
- *   y          [B, T, D] (dense) or [T, D] (packed), o_dtype, written; must not
- *              share memory with x, dt, B, C or z (KDA_ERR_INVALID_ARG)
+ *   y          [B, T, D] (dense) or [T, D] (packed), o_dtype, written
  *   mode       0 or KDA_SSM_SOFTPLUS
  * D a multiple of 8 * G, at most 2^20, S in {16, 32, 64}: others return
  * KDA_ERR_UNSUPPORTED.  Pointers 16-byte aligned.  Packed batches follow
@@ -489,8 +495,7 @@ kda_status kda_ssm_step(const void* x, long long ldx, const void* dt, long long 
  *              partial sums)
  * Sums over tokens, channels and sequences are added in a fixed order.  Packed
  * batches: gradient rows of no sequence and of skipped ones are zero, a skipped
- * sequence's grad_initial_state is grad_final_state.  The gradient buffers must
- * not alias the inputs.
+ * sequence's grad_initial_state is grad_final_state.
  */
 kda_status kda_ssm_bwd(const void* x, long long ldx, const void* dt, long long lddt, const float* A,
                        const void* B_, long long ldb, const void* C_, long long ldc, const float* skip,

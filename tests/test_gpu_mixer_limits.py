@@ -54,3 +54,35 @@ def test_every_bad_sequence_is_reported(N, T, D, states):
                 kda.kda_check()
             assert e.value.status == _lib.KDA_ERR_INVALID_ARG
             kda.kda_check()
+
+
+def test_neighbours_in_one_buffer():
+    """Tensors that touch without sharing memory are taken, and give what tensors of
+    their own do; so does a state updated in place."""
+    g = torch.Generator().manual_seed(2)
+    N, T, D, S = 2, 16, 64, 16
+
+    def arena(*shapes):
+        sizes = [torch.Size(s).numel() for s in shapes]
+        return [p.view(s) for p, s in zip(torch.empty(sum(sizes), device=DEV).split(sizes), shapes)]
+    w, A = torch.randn(D, 4, generator=g).to(DEV), -torch.rand(D, S, generator=g).to(DEV)
+    x, y, s0, sT = arena((N, T, D), (N, T, D), (N, 3, D), (N, 3, D))
+    x.copy_(torch.randn(N, T, D, generator=g))
+    s0.copy_(torch.randn(N, 3, D, generator=g))
+    want = kda.kda_conv_fwd(x.clone(), w, None, s0.clone())
+    kda.kda_conv_fwd(x, w, None, s0, y=y, final_state=sT)
+    assert torch.equal(y, want[0]) and torch.equal(sT, want[1])
+    kda.kda_conv_fwd(x, w, None, s0, y=y, final_state=s0)
+    assert torch.equal(y, want[0]) and torch.equal(s0, want[1])
+    x2, y, B, h, hT = arena((N, T, D), (N, T, D), (N, T, 1, S), (N, D, S), (N, D, S))
+    for t in (x2, B, h):
+        t.copy_(torch.randn(t.shape, generator=g))
+    want = kda.kda_ssm_fwd(x2.clone(), x, A, B, B, None, None, None, h.clone())
+    kda.kda_ssm_fwd(x2, x, A, B, B, None, None, None, h, y=y, final_state=hT)
+    assert torch.equal(y, want[0]) and torch.equal(hT, want[1])
+    kda.kda_ssm_fwd(x2, x, A, B, B, None, None, None, h, y=y, final_state=h)
+    assert torch.equal(y, want[0]) and torch.equal(h, want[1])
+    pool = torch.randn(N + 1, D, S, device=DEV)
+    with pytest.raises(kda.KdaError):
+        kda.kda_ssm_fwd(x2, x, A, B, B, None, None, None, pool[:N], final_state=pool[1:])
+    kda.kda_check()
