@@ -211,8 +211,8 @@ struct Seqs {
     long long tokens;
 
     __device__ __forceinline__ long long begin(int i) const { return cu ? (long long)cu[i] : (long long)i * T; }
-    // A sequence is used if its range lies in [0, tokens); an empty or
-    // decreasing pair has no tokens.
+    // A sequence is used if its range lies in [0, tokens); an empty pair has no
+    // tokens, a decreasing one none either (and is reported).
     __device__ __forceinline__ static bool inside(long long s, long long e, long long tokens)
     {
         return s >= 0 && e <= tokens;
@@ -237,8 +237,9 @@ __device__ __forceinline__ int find_sequence(const Seqs& q, long long t)
     return lo - 1;
 }
 
-// Reports every packed sequence whose range leaves the token axis (spread over
-// the whole grid).
+// Reports every packed sequence whose range leaves the token axis, and every
+// decreasing pair of boundaries: the rows around it are found by a search that
+// takes them in order (spread over the whole grid).
 __device__ __forceinline__ void flag_bad_sequences(const Seqs& q)
 {
     if (!q.cu) return;
@@ -246,7 +247,7 @@ __device__ __forceinline__ void flag_bad_sequences(const Seqs& q)
     long long i = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x;
     for (; i < q.n; i += nt) {
         const long long s = q.cu[i], e = q.cu[i + 1];
-        if (e > s && !Seqs::inside(s, e, q.tokens)) flag_bad_input();
+        if (e < s || (e > s && !Seqs::inside(s, e, q.tokens))) flag_bad_input();
     }
 }
 

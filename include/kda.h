@@ -359,7 +359,12 @@ kda_status kda_dplr_varlen_fwd_workspace_size(int N, int T, int H, int dk, int d
                                               size_t* bytes);
 
 /*
- * Shared memory, for the convolution and the scan below: what a call writes
+ * Packed batches of the convolution and the scan below follow kda_varlen_fwd's
+ * rules but for one: a decreasing pair of boundaries is reported by kda_check()
+ * (KDA_ERR_INVALID_ARG), and what the call then leaves in its outputs is not
+ * specified (nothing outside them is written).
+ *
+ * Shared memory, for the same calls: what a call writes
  * (y, states, gradients, workspace) must not share memory with what it reads or
  * with another of its outputs, or it returns KDA_ERR_INVALID_ARG.  Ranges of
  * addresses are compared; rows that lie apart count with what is between them.

@@ -86,3 +86,22 @@ def test_neighbours_in_one_buffer():
     with pytest.raises(kda.KdaError):
         kda.kda_ssm_fwd(x2, x, A, B, B, None, None, None, pool[:N], final_state=pool[1:])
     kda.kda_check()
+
+
+@pytest.mark.parametrize("cu", [[50, 100, 0, 50], [10, 0, 100], [0, 30, 20, 100], [0, 100, 99], [0] * 40 + [60, 40] + [100] * 40])
+def test_decreasing_boundaries_are_reported(cu):
+    """A token's sequence is searched for in order, so boundaries that decrease may leave
+    rows out (the first list: rows 0 to 50 of a convolution): never without a report."""
+    T, D = 100, 64
+    x, w = torch.randn(T, D, device=DEV), torch.randn(D, 4, device=DEV)
+    bc, A = torch.randn(T, 1, 16, device=DEV), -torch.rand(D, 16, device=DEV)
+    cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    for call in (lambda: kda.kda_conv_varlen_fwd(x, w, None, cu),
+                 lambda: kda.kda_conv_varlen_bwd(x, w, None, cu, None, x),
+                 lambda: kda.kda_ssm_varlen_fwd(x, x, A, bc, bc, cu),
+                 lambda: kda.kda_ssm_varlen_bwd(x, x, A, bc, bc, cu, None, None, None, None, x)):
+        call()
+        with pytest.raises(kda.KdaError) as e:
+            kda.kda_check()
+        assert e.value.status == _lib.KDA_ERR_INVALID_ARG
+        kda.kda_check()
