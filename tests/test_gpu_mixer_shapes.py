@@ -272,3 +272,70 @@ def test_gradients_beyond_32_bits():
     kda.kda_check()
     del x, dt, B, C, gy, whole, tail, part
     torch.cuda.empty_cache()
+
+
+def test_most_channels():
+    """2^20 channels, the limit, in one group: both operators, every direction."""
+    D, S, T = 1 << 20, 16, 2
+    args, grads, (x, w, b, s0, gy, gsT), cu = _conv_case([5, 2], D, 4, BF16, 31)
+    ch = np.arange(D) % P
+    y, sT = kda.kda_conv_varlen_fwd(x, w, b, cu, s0, o_dtype=F32)
+    got = kda.kda_conv_varlen_bwd(x, w, b, cu, s0, gy, gsT)
+    kda.kda_check()
+    conv_close(y, om.conv(*args)[0][:, ch], om.conv(*args, absolute=True)[0][:, ch], 32)
+    assert np.array_equal(f64(sT), om.conv(*args)[1][..., ch])
+    ref, mag = om.conv(*args, True, *grads), om.conv(*args, True, *grads, absolute=True)
+    for i, (a, r, m) in enumerate(zip(got, ref, mag)):
+        at = (ch,) if i in (1, 2) else (Ellipsis, ch)
+        conv_close(a, r[at], m[at], 64)
+    state = s0.clone()
+    y = kda.kda_conv_step(x[:2], w, b, state, o_dtype=F32)
+    one = (args[0][:2], *args[1:3], np.arange(3), args[4])
+    conv_close(y, om.conv(*one)[0][:, ch], om.conv(*one, absolute=True)[0][:, ch], 32)
+    p, cu, gy, gsT = _inputs([T], D, S, 1, F32, 32)
+    d = _lead(_dev(p), 1, T)
+    _check_fwd(p, cu, _fwd(d), {})
+    got = _bwd(d, gy.to(DEV).view(1, T, D), gsT.to(DEV))
+    kda.kda_check()
+    kw = dict({k: f64(v) for k, v in p.items()}, cu=cu, gy=f64(gy), gsT=f64(gsT))
+    for name, a, r, m in zip(GRADS, got, om.ssm(**kw), om.ssm(**kw, absolute=True)):
+        # sums over the channels: 32 in a tile, then the 32768 tiles in order
+        ssm_close(a, r, m, T, D // 32 + 32 if name in ("gB", "gC") else S, False, name)
+    state = d["s0"].clone()
+    y = kda.kda_ssm_step(d["x"][:, 0], d["dt"][:, 0], d["A"], d["B"][:, 0], d["C"][:, 0], state, d["skip"], d["z"][:, 0],
+                         d["dt_bias"])
+    first = {k: v[:1] if k in ("x", "dt", "z", "B", "C") else v for k, v in p.items()}
+    _check_fwd(first, np.array([0, 1]), (y, state), {})
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("N,T", [(65535, 2), (200000, 3)])
+def test_most_sequences(N, T):
+    """65535 packed sequences, the limit, are the same batch with equal lengths, bit for
+    bit; a dense batch may have more, and its last sequences are those of a call on them."""
+    D, S = 8, 16
+    p, _, gy, gsT = _inputs([T] * N, D, S, 1, BF16, 33)
+    d = _lead(_dev(p), N, T)
+    w, cs = torch.randn(D, 4, device=DEV), torch.randn(N, 3, D, device=DEV).to(BF16)
+    gyd, gsd, gcs = gy.to(DEV).view(N, T, D), gsT.to(DEV), torch.randn(N, 3, D, device=DEV)
+    ssm = (*_fwd(d), *_bwd(d, gyd, gsd))
+    conv = (*kda.kda_conv_fwd(d["x"], w, None, cs), *kda.kda_conv_bwd(d["x"], w, None, cs, gyd, gcs))
+    kda.kda_check()
+    if N == 65535:
+        cu = torch.arange(N + 1, dtype=torch.int32, device=DEV) * T
+        f = {k: v.reshape(N * T, *v.shape[2:]) if k in ("x", "dt", "z", "B", "C") else v for k, v in d.items()}
+        gyf = gyd.view(N * T, D)
+        ssm2 = (*_fwd(f, cu), *_bwd(f, gyf, gsd, cu))
+        conv2 = (*kda.kda_conv_varlen_fwd(f["x"], w, None, cu, cs),
+                 *kda.kda_conv_varlen_bwd(f["x"], w, None, cu, cs, gyf, gcs))
+        kda.kda_check()
+        for a, c in zip(ssm + conv, ssm2 + conv2):
+            assert (a is None and c is None) or torch.equal(a.reshape(c.shape), c)
+    n = 300
+    t = {k: v[-n:] if k in ("x", "dt", "z", "B", "C", "s0") else v for k, v in d.items()}
+    ssm3 = (*_fwd(t), *_bwd(t, gyd[-n:], gsd[-n:]))
+    for i in (0, 1, 2, 3, 5, 6, 8, 10):      # y, state, gx, gdt, gB, gC, gz, gs0
+        assert torch.equal(ssm[i][-n:], ssm3[i]), i
+    conv3 = (*kda.kda_conv_fwd(t["x"], w, None, cs[-n:]), *kda.kda_conv_bwd(t["x"], w, None, cs[-n:], gyd[-n:], gcs[-n:]))
+    for i in (0, 1, 2, 5):                   # y, state, gx, gs0
+        assert torch.equal(conv[i][-n:], conv3[i]), i
