@@ -10,10 +10,12 @@
 // W - 1 rows and the weights in registers, so no shared memory or synchronisation
 // is needed and the loads of the next tokens are in flight together.
 //
-// Measured (bf16 in and out, W = 4, SiLU, cold L2): 65536 x 2048 in 109 us, 4.9 TB/s
-// of 6.55 of a copy; 4096 x 2048 in 10.1 us.  Eight channels per thread halve the
-// requests but need 198 registers and half the warps: 320 us where four take 209.
-// Blocks of one token tile in a row instead of one channel block: the same.
+// Measured (bf16 in and out, W = 4, SiLU; here and below calls in a captured graph over
+// tensors of 600 MB in all, so out of the L2): 65536 x 2048 in 109 us, 4.9 TB/s of 6.55
+// of a copy; 16384 x 2048 in 31.9 us, 8192 x 2048 in 19.1, 4096 x 2048 in 11.2: about
+// 6 us and then 5.2 TB/s.  Eight channels per thread halve the requests but need 198
+// registers and half the warps: 320 us where four take 209.  Blocks of one token tile in
+// a row instead of one channel block: the same.
 #include "kda_mixer.cuh"
 
 namespace kda {
@@ -121,7 +123,10 @@ __global__ void __launch_bounds__(128, 5)
 conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ bias,
                 const T* s0, TO* __restrict__ y, T* sT, Seqs q, int D, int R, int ntiles)
 {
-    constexpr int U = sizeof(T) == 2 ? 8 : 4;   // 16 registers; fp32 with 8: 65536 x 2048 206 us for 175 (spills)
+    // 16 registers; fp32 with 8: 65536 x 2048 206 us for 175 (spills).  bf16 with SiLU spills a
+    // little at this bound: 4 bytes with 4 taps, 4, 20 and 32 with 2, 3 and 4 taps into fp32
+    // (139 us, 5.8 TB/s).
+    constexpr int U = sizeof(T) == 2 ? 8 : 4;
     typedef typename Raw<T>::quad Quad;
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * kV;
     flag_bad_sequences(q);   // by every block: the sequences are dealt to the whole grid
@@ -197,9 +202,9 @@ conv_fwd_kernel(const T* __restrict__ x, long long ldx, const float* __restrict_
 
 // One token per sequence: y from the state's rows and x; the state moves up by
 // one row.  A thread owns a channel vector of RN sequences, so that the weights
-// are read once for them and all their rows are in flight together.  1024 x 4096 in
-// bf16: 11.5 us for 75.5 MB, 6.6 TB/s, some of it from the L2; 16 sequences: 1.9 us,
-// a launch.
+// are read once for them and all their rows are in flight together.  bf16, W = 4: 1024 x
+// 4096 in 13.2 us for 67.1 MB, 5.1 TB/s, 4096 x 4096 46.4 us, 5.8 TB/s; 16 sequences:
+// 2.4 us, a launch.
 template <typename T, typename TO, int W, bool SILU, int RN>
 __global__ void __launch_bounds__(128)
 conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict__ w, const float* __restrict__ bias,
@@ -252,7 +257,8 @@ conv_step_kernel(const T* __restrict__ x, long long ldx, const float* __restrict
 // reaches is set by the loads in flight: four blocks of 128 registers per SM, and
 // every token's loads issued U tokens before they are used.  Both kernels: 8192 x 2048
 // 44 us, 3.8 TB/s; 65536 x 2048 271 us, 4.9 TB/s (with loads and sums in turn 48 and
-// 313; without the bound of 128 registers 56 and 280; five blocks 82 and 476).  Two
+// 313; without the bound of 128 registers 56 and 280; five blocks 82 and 476).  At that
+// bound 4 taps with SiLU spill 116 bytes in bf16 and 32 in fp32.  Two
 // channels per thread, tiles staged in shared memory by cp.async, and channel blocks
 // first in the grid measured slower.
 template <typename T, int W, bool SILU>
@@ -514,9 +520,9 @@ static int conv_threads(int vecs) { return vecs >= 128 ? 128 : (vecs + 31) / 32 
 
 // Tokens per tile of the backward pass: 128 where that leaves 256 threads per SM,
 // less halo and fewer partial sums; else half, down to 8; at most about 4096 partial
-// sums.  Both sides, D = 2048, bf16, us: T = 1024 with tiles of 8/16/32/128 14.7,
-// 16.7, 21.4, 55.7; T = 4096 with 16/32/64 33.5, 28.7, 38.5; T = 16384 with
-// 32/64/128 102, 90, 84 (all of them 0 to 12 % less since loads are issued ahead).
+// sums.  Both sides, D = 2048, bf16, us: T = 1024 with tiles of 8/16/32/128 15.3,
+// 16.9, 19.2, 41.8; T = 4096 with 16/32/64 33.4, 28.6, 34.0; T = 8192 with 32/64/128
+// 51.2, 44.4, 55.7; T = 16384 95.8, 82.3, 74.9; T = 65536 339, 288, 270.
 static int conv_bwd_tile(long long tokens, int D)
 {
     int r = 128;
@@ -532,9 +538,10 @@ static cudaError_t launch_conv_fwd(const ConvArgs& a, const void* s0, void* y, v
     const int nt = conv_threads(a.D / kV);
     const unsigned cb = (a.D / kV + nt - 1) / nt;
     // Tokens per tile: long tiles re-read less halo, short ones give enough threads:
-    // 32, halved to 8 until there are 256 threads per SM.  Both sides, D = 2048,
-    // bf16, us: T = 1024 with tiles of 8/16/32 4.4, 4.8, 6.8; T = 2048 7.8, 6.8, 8.7;
-    // T = 4096 11.7, 10.9, 10.5; T = 65536 139, 116, 109 (64: 108, 128: 115).
+    // 32, halved to 8 until there are 256 threads per SM.  Both sides, D = 2048, bf16,
+    // us: T = 1024 with tiles of 8/16/32 5.0, 5.6, 7.6; T = 2048 8.5, 7.3, 8.8; T = 4096
+    // 13.1, 11.8, 11.3; T = 8192 with 16/32/64 19.3, 19.1, 18.8 (2.8, 1.4 and 0.7 waves
+    // of blocks); T = 16384 34.3, 31.8, 34.0; T = 65536 121, 109, 106.
     int R = 32;
     while (R > 8 && (a.tokens / R) * cb * nt < 148LL * 256) R /= 2;
     const long long ntiles = (a.tokens + R - 1) / R;
@@ -561,8 +568,8 @@ static cudaError_t launch_conv_step(const ConvArgs& a, void* state, void* y, cud
             static_cast<const T*>(a.x), a.ldx, a.w, a.bias, static_cast<T*>(state), static_cast<TO*>(y), a.nseq, a.D);
     };
     // four sequences per thread share its weights once that leaves 128 threads per SM
-    // (D = 4096, bf16, one against four: 16 sequences 1.85 / 2.18 us, 128 3.24 / 2.84,
-    // 1024 13.9 / 11.5)
+    // (D = 4096, bf16, one against four, some of the state from the L2: 16 sequences
+    // 1.85 / 2.18 us, 128 3.24 / 2.84, 1024 13.9 / 11.5)
     if ((long long)a.nseq / 4 * cb * nt >= 148LL * 128)
         go(std::integral_constant<int, 4>{});
     else
@@ -589,7 +596,7 @@ static cudaError_t launch_conv_bwd(const ConvArgs& a, const void* s0, const floa
     return cudaGetLastError();
 }
 
-// Calls f.template operator()<T, TO, W, SILU>() for the call's types.
+// Calls f with the number of taps and whether there is a SiLU, as integral constants.
 template <typename F>
 static cudaError_t conv_dispatch_w(const ConvArgs& a, F&& f)
 {

@@ -233,14 +233,15 @@ ssm_walk_kernel(const SsmDev p, const WalkBwd wb)
 // output -- is done by one lane for one of the four sequences instead of by
 // every lane for all of them.  Bound by HBM: 256 x 4096 x 16 in 30 us, 143 MB, 4.8 TB/s
 // (59 us with RN = 1; the state read through the caches and B, C held from the start
-// 41); 2.2 us for one sequence, a launch.
+// 41); 2.2 us for one sequence, a launch.  The rate hardly climbs with the size (every
+// tensor out of the L2: 4.5 TB/s with 256 sequences, 4.7 with 512, 4.9 with 2048).
 template <typename T, int N, int RN>
 __global__ void __launch_bounds__(256)
 ssm_step_kernel(const SsmDev p, int n_seq)
 {
     static_assert(RN == 1 || RN == 4, "a row per lane of the smallest group, or one row");
     constexpr int L = N / 4;
-    const int f = blockIdx.x * 256 + threadIdx.x;   // 16-byte vector within one sequence's state (D N / 4 < 2^24)
+    const int f = blockIdx.x * 256 + threadIdx.x;   // 16-byte vector within one sequence's state (D N / 4 <= 2^24)
     const int d = f / L, l = f % L;
     if (d >= p.D) return;   // D is a multiple of 8 and 32 / L divides 8: whole warps leave
     const int lane = threadIdx.x & 31, group = lane / L * L;

@@ -496,7 +496,9 @@ constexpr long long kBwdTimeoutCycles = 1LL << 31;
 // has four warps, and an SM three (N = 16) or two of these.  All four launches,
 // D = 1024, bf16, 12 or 8 warps against 4, us: N = 16, 256 x 32 tokens 633 / 395,
 // 64 x 96 279 / 247, 32 x 256 303 / 309, 16 x 1024 591 / 670; N = 32, 64 x 64 340 / 307,
-// 32 x 256 552 / 572; N = 64, 64 x 64 791 / 728, 32 x 256 1368 / 1425.
+// 32 x 256 552 / 572; N = 64, 64 x 64 791 / 728, 32 x 256 1368 / 1425.  The host knows
+// the mean length only: with one long sequence among short ones four warps cost (512 x
+// 16 tokens and one of 8192 last 2232 / 2270, one of 4096 in the middle 1234 / 1643).
 constexpr int kNarrowTurns = 2;
 
 // Sequences are dealt to `slots` blocks per channel tile: enough to fill the 148 SMs

@@ -496,8 +496,9 @@ kda_status kda_ssm_step(const void* x, long long ldx, const void* dt, long long 
  *              where skip, z, dt_bias are given; NULL where they are not
  *   grad_initial_state [B, D, S] fp32, or NULL if not wanted
  *   workspace  at least kda_ssm_bwd_workspace_size() bytes, 256-byte aligned,
- *              contents need no initialisation (a state for every 4 or 8 tokens,
- *              partial sums)
+ *              contents need no initialisation (a state for every 8 tokens, or 4
+ *              for S = 64, and partial sums: about 12, 24 and 80 bytes per token and
+ *              channel for S = 16, 32 and 64)
  * Sums over tokens, channels and sequences are added in a fixed order.  Packed
  * batches: gradient rows of no sequence and of skipped ones are zero, a skipped
  * sequence's grad_initial_state is grad_final_state.
