@@ -95,15 +95,23 @@ def _types(x, o_dtype, y):
     return code, o_dtype, o_code
 
 
+_INT_MAX = (1 << 31) - 1   # the C ABI's int: ctypes drops the bits above without a word
+
+
 def _lead(x, dims):
-    if x.dim() != dims:
-        raise ValueError(f"x has {x.dim()} dimensions, expected {dims}")
-    return x.shape
+    shape = x.shape
+    if len(shape) != dims:
+        raise ValueError(f"x has {len(shape)} dimensions, expected {dims}")
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX:
+        raise ValueError(f"x has shape {tuple(shape)}: at most {_INT_MAX} sequences and tokens each")
+    return shape
 
 
 def _packed(cu_seqlens, x):
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected (N + 1,)")
+    if cu_seqlens.shape[0] > _INT_MAX:
+        raise ValueError(f"cu_seqlens has {cu_seqlens.shape[0] - 1} sequences, at most 65535 are supported")
     _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, x.get_device())
     return cu_seqlens.shape[0] - 1
 

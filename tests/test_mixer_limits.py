@@ -84,3 +84,32 @@ def test_ssm_outputs_that_share_memory():
     bwd = ins + tuple(k * F for k in range(9, 21)) + (2, 9, D, S, G, BF16, 1, 21 * F, size.value, None)
     _clashes("kda_ssm_bwd", bwd, {16: 2 * act, 17: 2 * act, 18: A, 19: 2 * bc, 20: 2 * bc, 21: v, 22: 2 * act, 23: v,
                                   24: st, 32: size.value}, {**sizes, 13: st, 14: 2 * act, 15: st})
+
+
+def test_sizes_beyond_an_int_are_refused():
+    """2^32 + 5 tokens are not 5 (on the meta device: nothing is allocated)."""
+    import torch
+    import gated_delta_rule_133_b200 as kda
+
+    def meta(*shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+    big, w, A = (1 << 32) + 5, meta(8, 4), meta(8, 16)
+    cu = meta(big + 1, dtype=torch.int32)
+    for x in (meta(1, big, 8), meta(big, 1, 8)):
+        bc = meta(*x.shape[:2], 1, 16)
+        for call in (lambda: kda.kda_conv_fwd(x, w), lambda: kda.kda_conv_bwd(x, w, None, None, x),
+                     lambda: kda.kda_ssm_fwd(x, x, A, bc, bc),
+                     lambda: kda.kda_ssm_bwd(x, x, A, bc, bc, None, None, None, None, x)):
+            with pytest.raises(ValueError, match="at most 2147483647"):
+                call()
+    x, bc = meta(big, 8), meta(big, 1, 16)
+    for call in (lambda: kda.kda_conv_step(x, w, None, meta(big, 3, 8)), lambda: kda.kda_conv_varlen_fwd(x, w, None, cu),
+                 lambda: kda.kda_ssm_step(x, x, A, bc, bc, meta(big, 8, 16)),
+                 lambda: kda.kda_ssm_varlen_fwd(x, x, A, bc, bc, cu)):
+        with pytest.raises(ValueError, match="at most 2147483647"):
+            call()
+    x, bc = meta(9, 8), meta(9, 1, 16)
+    for call in (lambda: kda.kda_conv_varlen_fwd(x, w, None, cu), lambda: kda.kda_ssm_varlen_fwd(x, x, A, bc, bc, cu),
+                 lambda: kda.kda_conv_varlen_bwd(x, w, None, cu, None, x)):
+        with pytest.raises(ValueError, match="at most 65535"):
+            call()
