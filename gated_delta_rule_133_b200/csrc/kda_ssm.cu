@@ -55,7 +55,8 @@ __device__ __forceinline__ void bar_arrive(int id, int threads)
 // (channel, state, token) 11.5 instructions are issued (62 % of the slots at full
 // load) and 3.6 words per lane leave shared memory (76 % of its cycles), so no single
 // unit is full but the two together are.  Four warps of 8 channels and 120 registers:
-// with 96 (five blocks) the decays spill, 20 cycles for 18; W = 8 is 2 % faster at
+// with 96 (five blocks) the decays spill, 20 cycles for 18 (at 128, N = 64 spills 8 bytes
+// in bf16 and 24 in fp32, the backward pass's form 16 and 64); W = 8 is 2 % faster at
 // 512 blocks and 5 % slower at 2048, W = 3, 5, 6 slower at both; twice the states per
 // lane save shared memory and wait at the hand-over (275 cycles), 20 to 22 cycles; two
 // states per lane 197 us; B and C in fp32 8 % slower; the time split into groups with
